@@ -58,7 +58,8 @@ typedef enum {
     RA_ERR_INVALID_ARG = -1,
     RA_ERR_UNSUPPORTED = -2,
     RA_ERR_CUDA = -3,
-    RA_ERR_DEVICE_TIMEOUT = -4
+    RA_ERR_DEVICE_TIMEOUT = -4,
+    RA_ERR_BAD_PAGE = -5
 } ra_status;
 
 /*
@@ -319,6 +320,125 @@ int ring_attn_fwd_emulated(const ra_bf16 *q, const ra_bf16 *k, const ra_bf16 *v,
 int attn_merge_partials(const float *o_a, const float *lse_a, const float *o_b, const float *lse_b,
                         float *o_out, float *lse_out, int B, int H, int S, int d, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Paged key/value cache: serving with contexts that grow token by token.
+ *
+ * K and V live in two pools of `num_pages` pages of `page_size` tokens; the
+ * contexts of many requests share them.  Key c of request i is row
+ * c % page_size of page block_table[i][c / page_size].  A step of a serving
+ * loop is
+ *     paged_kv_plan     where the new tokens go: pages, slots, lengths
+ *     paged_kv_append   (every layer) their K and V rows into the pools
+ *     paged_attn_fwd    (every layer) their attention over their contexts
+ * and none of the three reads anything on the host: a step can be captured
+ * into a CUDA graph and replayed as the lengths grow.
+ *
+ * Pools: row (page, token, head) starts at element page * strides[0] +
+ * token * strides[1] + head * strides[2]; its d elements are contiguous.
+ * NULL strides are the contiguous [num_pages, page_size, H_kv, d] layout;
+ * {H_kv * page_size * d, d, page_size * d} is [num_pages, H_kv, page_size,
+ * d].  Strides are positive multiples of 8 elements below 2^35 (those of a
+ * dimension of extent 1 are not used).  page_size is a multiple of 8 (else
+ * RA_ERR_UNSUPPORTED) and num_pages * page_size below 2^31.
+ * Elements are bf16 (RA_BF16) or fp16 (RA_FP16).
+ *
+ * What these calls read on the device cannot be checked on the host.  A page
+ * or slot outside the pool is never followed: its keys read as rows of
+ * zeros, its tokens are not appended, and ring_attn_check_status then
+ * reports RA_ERR_BAD_PAGE.  Lengths are cut to what the tables and buffers
+ * hold.
+ * ------------------------------------------------------------------------ */
+typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
+
+/*
+ * The bookkeeping of one step, for n requests (n <= 8192, else
+ * RA_ERR_UNSUPPORTED).
+ *   seq_lens     [n] int32 tokens in the cache.
+ *   new_lens     [n] int32 tokens to add; 0 leaves a request as it is, a
+ *                negative value ends it and gives its pages back.
+ *   block_table  [n, max_pages] int32, row i at i * table_stride elements.
+ *                The pages of the cached tokens are read, new ones are
+ *                written behind them; no other entry is touched.
+ *   free_list    [num_pages] int32, a stack of free page numbers: the first
+ *                counts[0] entries are free, the last of them goes first.
+ *   counts       [2] int32; counts[0] the number of free pages.
+ *   seq_lens_out [n] int32 lengths after the step.
+ *   cu_q         [n + 1] int32 where each request's new tokens start in the
+ *                step's token axis: the sums of max(new_lens, 0).
+ *   slots        [tokens] int32 for each new token page * page_size +
+ *                offset; -1 for tokens of requests that were not granted
+ *                and behind the last token.
+ *   counts_out   [2] int32: free pages after the step; requests not granted.
+ * Ended requests give their pages back first, in order; then requests take
+ * theirs in order.  A request whose new tokens do not fit its table row or
+ * the slots is not granted, and from the first one for whose pages the stack
+ * is too short no request that needs pages is.  A request that is not
+ * granted keeps its length, its pages and its tokens' places in cu_q; try it
+ * again when there are pages.
+ * seq_lens_out may be seq_lens and counts_out may be counts (a loop's state,
+ * updated in place); otherwise buffers do not overlap.  Where they are not
+ * updated in place the call can be repeated with the same result.
+ * n * max_pages and num_pages are at most 2^30, max_pages * page_size below
+ * 2^31.
+ */
+int paged_kv_plan(const int *seq_lens, const int *new_lens, int n, int *block_table,
+                  long long table_stride, int max_pages, int *free_list, int num_pages,
+                  const int *counts, int page_size, int tokens, int *seq_lens_out, int *cu_q,
+                  int *slots, int *counts_out, void *stream);
+
+/*
+ * New K and V rows into the pools: row (t, h) of k goes to slot slots[t] of
+ * head h, for every slot that is not -1.  The slots of one call are
+ * different from one another (those of paged_kv_plan are); of two equal ones
+ * either row, or parts of both, may be kept.
+ *   k, v         [tokens, H_kv, d] rows, placed by their strides {token,
+ *                head}; NULL = contiguous.
+ *   d            64 or 128.
+ */
+int paged_kv_append(const void *k, const long long *k_strides, const void *v,
+                    const long long *v_strides, void *k_cache, const long long *k_cache_strides,
+                    void *v_cache, const long long *v_cache_strides, const int *slots, int tokens,
+                    int H_kv, int d, int num_pages, int page_size, void *stream);
+
+/*
+ * Bytes of device workspace paged_attn_fwd needs, whatever the lengths; 0
+ * for empty or invalid shapes.
+ */
+size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d);
+
+/*
+ * Attention of new tokens over their requests' contexts, exactly as
+ * ring_attn_fwd_gqa computes it for the last rows of each context.
+ *   q            [tokens, H, d] the new tokens of all requests, one request
+ *                after the other; request i's are rows cu_q[i] .. cu_q[i+1].
+ *                Rows are placed by q_strides {token, head}; NULL =
+ *                contiguous.
+ *   block_table, seq_lens, cu_q  as paged_kv_plan leaves them: seq_lens
+ *                counts the new tokens too, and their K and V are in the
+ *                pools already.
+ *   o            [tokens, H, d], placed by o_strides; lse [H, tokens] fp32
+ *                (natural log).  Rows of no request are not written.
+ *   causal       1: token t of q_i sees keys c <= len_i - q_i + t.
+ *                0: every key of its request.
+ *                A row that sees no key gives O = 0 and LSE = -inf, the
+ *                identity of attn_merge_partials.
+ *   scale        finite and above 0.
+ *   max_q        an upper bound of the new tokens of one request, for the
+ *                choice of kernels only: results do not depend on it.
+ *   dtype        RA_BF16 or RA_FP16, of q, the pools and o.
+ *   H / H_kv     a whole number up to 128 (more: RA_ERR_UNSUPPORTED).
+ *   workspace    paged_attn_workspace_size bytes, 256-byte aligned, of any
+ *                contents; calls that may run at the same time need one each.
+ * Keys behind a row's last one do not reach it, whatever they hold.
+ */
+int paged_attn_fwd(const void *q, const long long *q_strides, const void *k_cache,
+                   const long long *k_cache_strides, const void *v_cache,
+                   const long long *v_cache_strides, const int *block_table, long long table_stride,
+                   const int *seq_lens, const int *cu_q, void *o, const long long *o_strides,
+                   float *lse, int dtype, int n, int tokens, int H, int H_kv, int d, int num_pages,
+                   int page_size, int max_pages, int max_q, int causal, float scale,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * The chunk-level ring schedule the kernels follow, on the host.  For query
  * chunk i (0 <= i < P) writes, in ring order t = 0, 1, ..., the visited KV
@@ -333,7 +453,8 @@ int ring_attn_schedule(int P, int causal, int i, int *out_j, int *out_kind, int 
 /*
  * Synchronizes `stream`, then reads and clears the current device's status
  * word.  RA_OK if no kernel reported a problem since the last check,
- * RA_ERR_DEVICE_TIMEOUT if a bounded wait ran out, RA_ERR_CUDA if the
+ * RA_ERR_DEVICE_TIMEOUT if a bounded wait ran out, RA_ERR_BAD_PAGE if a
+ * paged call met a page or slot outside its pool, RA_ERR_CUDA if the
  * stream reported an error.
  */
 int ring_attn_check_status(void *stream);
@@ -390,7 +511,9 @@ int ring_attn_trace_visits(int *buf, long long capacity);
  * bracketed by a pair of CUDA events on its launch stream.
  * ring_attn_profile_read synchronizes on the recorded events and returns,
  * for the kernel named (one of "ring_fwd_kernel", "ring_bwd_kernel",
- * "bwd_prep_kernel", "dq_convert_kernel", "merge_partials_kernel"), the
+ * "bwd_prep_kernel", "dq_convert_kernel", "merge_partials_kernel",
+ * "f32_to_bf16_kernel", "paged_plan_kernel", "paged_append_kernel",
+ * "paged_rows_kernel"), the
  * number of launches and their summed device time in milliseconds since
  * the last ring_attn_profile_reset.  Host-side state, process-wide; not for
  * use inside CUDA graph capture.  RA_ERR_INVALID_ARG for an unknown name.

@@ -5,6 +5,9 @@
     o, lse = ring_attn_fwd(q, k, v, P=4, causal=True)
     dq, dk, dv = ring_attn_bwd(q, k, v, o, lse, dO, P=4, causal=True)
 
+and, for contexts that grow token by token, a paged key/value cache:
+paged_kv_plan, paged_kv_append and paged_attn_fwd.
+
 Torch is used for device memory and streams only; every step runs in the
 library's kernels.  Build the library with
 ``python -m long_context_exact_ring_gb300.build``.
@@ -12,6 +15,7 @@ library's kernels.  Build the library with
 from ._binding import (  # noqa: F401
     EXPORTED,
     LIB_PATH,
+    RA_ERR_BAD_PAGE,
     RA_ERR_CUDA,
     RA_ERR_DEVICE_TIMEOUT,
     RA_ERR_INVALID_ARG,
@@ -39,4 +43,10 @@ from ._binding import (  # noqa: F401
     set_wait_limit_ns,
     status_string,
     trace_visits,
+)
+from ._paged import (  # noqa: F401
+    paged_attn_fwd,
+    paged_attn_workspace_size,
+    paged_kv_append,
+    paged_kv_plan,
 )

@@ -23,6 +23,7 @@ RA_ERR_INVALID_ARG = -1
 RA_ERR_UNSUPPORTED = -2
 RA_ERR_CUDA = -3
 RA_ERR_DEVICE_TIMEOUT = -4
+RA_ERR_BAD_PAGE = -5
 
 EXPORTED = (
     "ring_attn_fwd",
@@ -40,6 +41,10 @@ EXPORTED = (
     "ring_attn_bwd",
     "ring_attn_bwd_noalloc",
     "attn_merge_partials",
+    "paged_kv_plan",
+    "paged_kv_append",
+    "paged_attn_fwd",
+    "paged_attn_workspace_size",
     "ring_attn_schedule",
     "ring_attn_check_status",
     "ring_attn_status_string",
@@ -113,6 +118,15 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.ring_attn_bwd_noalloc.restype = i
         lib.attn_merge_partials.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, vp]
         lib.attn_merge_partials.restype = i
+        lib.paged_kv_plan.argtypes = [vp, vp, i, vp, ctypes.c_longlong, i, vp, i, vp, i, i, vp, vp, vp, vp, vp]
+        lib.paged_kv_plan.restype = i
+        lib.paged_kv_append.argtypes = [vp, llp, vp, llp, vp, llp, vp, llp, vp, i, i, i, i, i, vp]
+        lib.paged_kv_append.restype = i
+        lib.paged_attn_workspace_size.argtypes = [i, i, i, i, i]
+        lib.paged_attn_workspace_size.restype = sz
+        lib.paged_attn_fwd.argtypes = [vp, llp, vp, llp, vp, llp, vp, ctypes.c_longlong, vp, vp, vp, llp, vp,
+                                       i, i, i, i, i, i, i, i, i, i, i, f, vp, sz, vp]
+        lib.paged_attn_fwd.restype = i
         lib.ring_attn_schedule.argtypes = [i, i, i, ip, ip, i]
         lib.ring_attn_schedule.restype = i
         lib.ring_attn_check_status.argtypes = [vp]
@@ -477,7 +491,8 @@ def trace_visits(buf=None) -> None:
 
 
 KERNELS = ("ring_fwd_kernel", "ring_bwd_kernel", "bwd_prep_kernel", "dq_convert_kernel",
-           "merge_partials_kernel", "f32_to_bf16_kernel")
+           "merge_partials_kernel", "f32_to_bf16_kernel", "paged_plan_kernel", "paged_append_kernel",
+           "paged_rows_kernel")
 
 
 def profile_enable(on: bool = True) -> None:

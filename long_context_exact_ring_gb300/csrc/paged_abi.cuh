@@ -1,0 +1,221 @@
+// paged_abi.cuh -- the C-ABI boundary of the paged key/value cache: argument
+// checks and launches.  Part of ring_attn.cu, whose per-device state and
+// error reporting it uses.
+#pragma once
+
+namespace {
+
+// Strides of `count` dimensions of the given extents, or those of the
+// contiguous layout when the caller passes NULL.  Usable are positive
+// multiples of 8 elements (16 bytes) below 2^35; the stride of an extent-1
+// dimension is never used and becomes 0.
+bool paged_strides(long long* out, const long long* given, const long long* contiguous, const int* extents,
+                   int count)
+{
+    for (int x = 0; x < count; ++x) {
+        const long long st = given ? given[x] : contiguous[x];
+        if (extents[x] <= 1) out[x] = 0;
+        else if (st <= 0 || st % 8 != 0 || st >= (1ll << 35)) return false;
+        else out[x] = st;
+    }
+    return true;
+}
+
+bool row_strides(long long* out, const long long* given, int tokens, int heads, int d)
+{
+    const long long contiguous[2] = {(long long)heads * d, d};
+    const int extents[2] = {tokens, heads};
+    return paged_strides(out, given, contiguous, extents, 2);
+}
+
+bool pool_strides(ra::paged::PoolLayout* out, const long long* given, int pages, int page_size, int heads, int d)
+{
+    const long long contiguous[3] = {(long long)page_size * heads * d, (long long)heads * d, d};
+    const int extents[3] = {pages, page_size, heads};
+    long long st[3];
+    if (!paged_strides(st, given, contiguous, extents, 3)) return false;
+    *out = {st[0], st[1], st[2]};
+    return true;
+}
+
+int check_pool(int num_pages, int page_size, int H_kv, int d)
+{
+    if (num_pages < 1 || page_size < 1 || H_kv < 1) return RA_ERR_INVALID_ARG;
+    if (page_size % 8 != 0 || (d != 64 && d != 128)) return RA_ERR_UNSUPPORTED;
+    if ((long long)num_pages * page_size >= (1ll << 31)) return RA_ERR_UNSUPPORTED;
+    return RA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Once per device, before the first launch of a kernel with this much
+// dynamic shared memory.
+template <typename Kernel>
+int allow_smem(Kernel kernel, int bytes)
+{
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    return e == cudaSuccess ? RA_OK : fail_cuda(e, "cudaFuncSetAttribute");
+}
+
+}  // namespace
+
+extern "C" {
+
+int paged_kv_plan(const int* seq_lens, const int* new_lens, int n, int* block_table, long long table_stride,
+                  int max_pages, int* free_list, int num_pages, const int* counts, int page_size, int tokens,
+                  int* seq_lens_out, int* cu_q, int* slots, int* counts_out, void* stream)
+{
+    if (n < 0 || tokens < 0) return RA_ERR_INVALID_ARG;
+    const int rc = check_pool(num_pages, page_size, 1, 64);
+    if (rc != RA_OK) return rc;
+    if (max_pages < 1 || table_stride < max_pages) return RA_ERR_INVALID_ARG;
+    if (n > ra::paged::kMaxRequests || (long long)n * max_pages > (1ll << 30) || num_pages > (1 << 30) ||
+        (long long)max_pages * page_size >= (1ll << 31))
+        return RA_ERR_UNSUPPORTED;
+    if (n == 0 && tokens == 0) return RA_OK;
+    if (!free_list || !counts || !counts_out || !cu_q || (tokens > 0 && !slots) ||
+        (n > 0 && (!seq_lens || !new_lens || !block_table || !seq_lens_out)))
+        return RA_ERR_INVALID_ARG;
+    const void* all[] = {seq_lens, new_lens, block_table, free_list, counts, seq_lens_out, cu_q, slots, counts_out};
+    for (const void* x : all)
+        if (!aligned4(x)) return RA_ERR_INVALID_ARG;
+    DeviceState* st = nullptr;
+    int e = device_state(&st);
+    if (e != RA_OK) return e;
+    ra::paged::PlanParams p{seq_lens,     new_lens, block_table, table_stride, free_list, counts, seq_lens_out,
+                            cu_q,         slots,    counts_out,  n,            max_pages, num_pages, page_size,
+                            tokens};
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const size_t smem = ra::paged::plan_smem(n);
+    if (smem > 48 * 1024) {
+        e = allow_smem(ra::paged::paged_plan_kernel, (int)ra::paged::plan_smem(ra::paged::kMaxRequests));
+        if (e != RA_OK) return e;
+    }
+    ra::prof::Scope ps(ra::prof::kPagedPlan, s);
+    ra::paged::paged_plan_kernel<<<1, ra::paged::kPlanThreads, smem, s>>>(p);
+    ps.done();
+    const cudaError_t ce = cudaGetLastError();
+    return ce == cudaSuccess ? RA_OK : fail_cuda(ce, "paged_plan_kernel launch");
+}
+
+int paged_kv_append(const void* k, const long long* k_strides, const void* v, const long long* v_strides,
+                    void* k_cache, const long long* k_cache_strides, void* v_cache,
+                    const long long* v_cache_strides, const int* slots, int tokens, int H_kv, int d, int num_pages,
+                    int page_size, void* stream)
+{
+    if (tokens < 0) return RA_ERR_INVALID_ARG;
+    int rc = check_pool(num_pages, page_size, H_kv, d);
+    if (rc != RA_OK) return rc;
+    long long ks[2], vs[2];
+    ra::paged::PoolLayout lk, lv;
+    if (!row_strides(ks, k_strides, tokens, H_kv, d) || !row_strides(vs, v_strides, tokens, H_kv, d) ||
+        !pool_strides(&lk, k_cache_strides, num_pages, page_size, H_kv, d) ||
+        !pool_strides(&lv, v_cache_strides, num_pages, page_size, H_kv, d))
+        return RA_ERR_INVALID_ARG;
+    if (tokens == 0) return RA_OK;
+    if (!k || !v || !k_cache || !v_cache || !slots) return RA_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned4(slots))
+        return RA_ERR_INVALID_ARG;
+    if (H_kv > (1 << 20)) return RA_ERR_UNSUPPORTED;
+    DeviceState* st = nullptr;
+    if ((rc = device_state(&st)) != RA_OK) return rc;
+    const int vec_shift = d == 128 ? 4 : 3;
+    const long long pieces = ((long long)tokens * H_kv) << vec_shift;
+    const long long blocks = std::min((pieces + 255) / 256, (long long)st->num_sms * 16);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    ra::prof::Scope ps(ra::prof::kPagedAppend, s);
+    ra::paged::paged_append_kernel<<<(unsigned)blocks, 256, 0, s>>>(
+        static_cast<const uint16_t*>(k), ks[0], ks[1], static_cast<const uint16_t*>(v), vs[0], vs[1],
+        static_cast<uint16_t*>(k_cache), lk, static_cast<uint16_t*>(v_cache), lv, slots, tokens, H_kv, vec_shift,
+        page_size, num_pages * page_size, st->status);
+    ps.done();
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? RA_OK : fail_cuda(e, "paged_append_kernel launch");
+}
+
+size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d)
+{
+    if (n <= 0 || tokens <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
+    return 256;
+}
+
+int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cache, const long long* k_cache_strides,
+                   const void* v_cache, const long long* v_cache_strides, const int* block_table,
+                   long long table_stride, const int* seq_lens, const int* cu_q, void* o, const long long* o_strides,
+                   float* lse, int dtype, int n, int tokens, int H, int H_kv, int d, int num_pages, int page_size,
+                   int max_pages, int max_q, int causal, float scale, void* workspace, size_t workspace_bytes,
+                   void* stream)
+{
+    if (n < 0 || tokens < 0 || H < 1 || max_q < 0 || (causal != 0 && causal != 1)) return RA_ERR_INVALID_ARG;
+    if (dtype != RA_BF16 && dtype != RA_FP16) return RA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return RA_ERR_INVALID_ARG;
+    int rc = check_pool(num_pages, page_size, H_kv, d);
+    if (rc != RA_OK) return rc;
+    if (H % H_kv != 0 || max_pages < 1 || table_stride < max_pages) return RA_ERR_INVALID_ARG;
+    if (H / H_kv > 128 || H > (1 << 20) || (long long)H * tokens >= (1ll << 31) ||
+        (long long)max_pages * page_size >= (1ll << 31))
+        return RA_ERR_UNSUPPORTED;
+    long long qs[2], os[2];
+    ra::paged::PoolLayout lk, lv;
+    if (!row_strides(qs, q_strides, tokens, H, d) || !row_strides(os, o_strides, tokens, H, d) ||
+        !pool_strides(&lk, k_cache_strides, num_pages, page_size, H_kv, d) ||
+        !pool_strides(&lv, v_cache_strides, num_pages, page_size, H_kv, d))
+        return RA_ERR_INVALID_ARG;
+    if (n == 0 || tokens == 0) return RA_OK;
+    if (!q || !k_cache || !v_cache || !block_table || !seq_lens || !cu_q || !o || !lse || !workspace)
+        return RA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned4(block_table) ||
+        !aligned4(seq_lens) || !aligned4(cu_q) || !aligned4(lse) || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+        workspace_bytes < paged_attn_workspace_size(n, tokens, H, H_kv, d))
+        return RA_ERR_INVALID_ARG;
+    DeviceState* st = nullptr;
+    if ((rc = device_state(&st)) != RA_OK) return rc;
+
+    ra::paged::AttnParams p;
+    p.q = static_cast<const uint16_t*>(q);
+    p.q_tok = qs[0];
+    p.q_head = qs[1];
+    p.kc = static_cast<const uint16_t*>(k_cache);
+    p.lk = lk;
+    p.vc = static_cast<const uint16_t*>(v_cache);
+    p.lv = lv;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.seq_lens = seq_lens;
+    p.cu_q = cu_q;
+    p.o = static_cast<uint16_t*>(o);
+    p.o_tok = os[0];
+    p.o_head = os[1];
+    p.lse = lse;
+    p.n = n;
+    p.tokens = tokens;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.page_size = page_size;
+    p.page_shift = -1;
+    for (int x = 0; x < 31; ++x)
+        if (page_size == (1 << x)) p.page_shift = x;
+    p.kv_heads = H_kv;
+    p.group = H / H_kv;
+    p.causal = causal;
+    p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+    p.status = st->status;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    auto launch = [&](auto kernel, int smem) {
+        const int e = allow_smem(kernel, smem);
+        if (e != RA_OK) return e;
+        ra::prof::Scope ps(ra::prof::kPagedRows, s);
+        kernel<<<st->num_sms, ra::paged::rows::kThreads, smem, s>>>(p);
+        ps.done();
+        const cudaError_t ce = cudaGetLastError();
+        return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged_rows_kernel launch");
+    };
+    namespace pr = ra::paged::rows;
+    if (d == 128)
+        return dtype == RA_FP16 ? launch(pr::paged_rows_kernel<128, true>, pr::Cfg<128>::kSmemBytes)
+                                : launch(pr::paged_rows_kernel<128, false>, pr::Cfg<128>::kSmemBytes);
+    return dtype == RA_FP16 ? launch(pr::paged_rows_kernel<64, true>, pr::Cfg<64>::kSmemBytes)
+                            : launch(pr::paged_rows_kernel<64, false>, pr::Cfg<64>::kSmemBytes);
+}
+
+}  // extern "C"

@@ -1,0 +1,424 @@
+// paged_attn.cuh -- attention of new tokens over a paged key/value cache.
+//
+// Request i has len_i cached tokens, the last q_i of them new.  New token t
+// sits at position len_i - q_i + t and attends to the keys c <= position
+// (causal) or to all len_i keys:
+//     s_c = scale <q, k_c>,  LSE = ln sum_c exp(s_c),  O = sum_c exp(s_c - LSE) v_c,
+// and a row without keys gives O = 0, LSE = -inf.  Query head h reads
+// key/value head h / group.  Key c lies in page block_table[i, c / page_size].
+//
+// The new tokens of a request that share a key/value head -- `group` query
+// heads of each token -- are packed into rows r = token * group + head, so one
+// pass over the keys serves all of them.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "paged_cache.cuh"
+
+namespace ra {
+namespace paged {
+
+struct AttnParams {
+    const uint16_t* q;
+    long long q_tok, q_head;
+    const uint16_t* kc;
+    PoolLayout lk;
+    const uint16_t* vc;
+    PoolLayout lv;
+    const int* table;
+    long long table_stride;
+    const int* seq_lens;
+    const int* cu_q;
+    uint16_t* o;
+    long long o_tok, o_head;
+    float* lse;              // [heads, tokens]
+    int n, tokens, max_pages, num_pages, page_size, page_shift;   // page_shift < 0: not a power of two
+    int kv_heads, group, causal;
+    float scale_log2;
+    uint32_t* status;
+};
+
+__device__ __forceinline__ Request load_request(const AttnParams& p, int i)
+{
+    return cut_request(p.cu_q[i], p.cu_q[i + 1], p.seq_lens[i], p.tokens, p.max_pages, p.page_size);
+}
+
+// The operand types: bf16 or fp16 products with fp32 accumulation.  kShift
+// moves the reference of the exponentials: the weights 2^(x - m + kShift)
+// are rounded to the operand type for the product with V, and fp16 would
+// lose those below 2^-24; with the row maximum at 2^15 it keeps them down
+// to 2^-39 of the largest.  bf16 has fp32's range and needs no shift.
+template <bool kHalf> struct Operand;
+
+template <> struct Operand<false> {
+    static constexpr float kShift = 0.f;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return pack_bf16x2(lo, hi); }
+    static __device__ __forceinline__ bool nonfinite(uint32_t x)
+    {
+        return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+    }
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                     "{%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+template <> struct Operand<true> {
+    static constexpr float kShift = 15.f;
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi)
+    {
+        uint32_t r;
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
+    static __device__ __forceinline__ bool nonfinite(uint32_t x)
+    {
+        return (x & 0x7c00u) == 0x7c00u || (x & 0x7c000000u) == 0x7c000000u;
+    }
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+    {
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+                     "{%8, %9}, {%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+};
+
+// max(a, b), NaN if either is: a NaN score has to reach its row's result.
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take)
+{
+    const uint32_t bytes = take ? 16u : 0u;   // 0: the 16 bytes are filled with zeros, src is not read
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+namespace rows {
+
+constexpr int kRows = 16;        // packed rows of a tile: one m16n8k16 operand
+constexpr int kKeys = 16;        // keys of a warp's step
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+
+template <int D>
+struct Cfg {
+    static constexpr int kChunkBytes = kKeys * D * 2;              // a warp's K (or V) of one step
+    static constexpr int kMergeBytes = kRows * D * 4 + 2 * kRows * 4;
+    static constexpr int kWarpBytes = 2 * kChunkBytes > kMergeBytes ? 2 * kChunkBytes : (kMergeBytes + 127) / 128 * 128;
+    static constexpr int kSmemBytes = kWarps * kWarpBytes;
+};
+
+// One warp's running state of a tile: 16 rows, of which a thread holds two.
+template <int D>
+struct State {
+    float m[2], l[2];
+    float acc[D / 8][4];
+};
+
+// One block per (request, key/value head, tile of 16 packed rows), taken in
+// turn.  Every warp streams its own 16 keys out of each 128 through its own
+// corner of shared memory, with no barrier between warps, and keeps its own
+// softmax state; the states of the eight warps are merged at the end.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParams p)
+{
+    using C = Cfg<D>;
+    using Op = Operand<kHalf>;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ long long s_scratch[kWarps + 1];
+    __shared__ int s_item[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, t4 = lane & 3;
+    uint8_t* my = smem_raw + warp * C::kWarpBytes;
+    const uint32_t sK = smem_u32(my), sV = sK + C::kChunkBytes;
+
+    // tiles of all requests before each thread's share of them
+    const int per = (p.n + kThreads - 1) / kThreads;
+    const int i0 = min(p.n, tid * per), i1 = min(p.n, i0 + per);
+    auto tiles_of = [&](int i) {
+        const Request r = load_request(p, i);
+        return ((long long)r.q * p.group + kRows - 1) / kRows * p.kv_heads;
+    };
+    long long mine = 0, total;
+    for (int i = i0; i < i1; ++i) mine += tiles_of(i);
+    const long long before = block_exclusive_sum(mine, s_scratch, &total);
+
+    for (long long item = blockIdx.x; item < total; item += gridDim.x) {
+        __syncthreads();
+        if (before <= item && item < before + mine) {
+            long long x = item - before;
+            int i = i0;
+            for (long long c; x >= (c = tiles_of(i)); ++i) x -= c;
+            s_item[0] = i;
+            s_item[1] = (int)x;
+        }
+        __syncthreads();
+        const int req = s_item[0];
+        const Request r = load_request(p, req);
+        const int tiles = (r.q * p.group + kRows - 1) / kRows;
+        const int kvh = s_item[1] / tiles, row0 = (s_item[1] - kvh * tiles) * kRows;
+        const int rows = min(kRows, r.q * p.group - row0);
+        const int* table = p.table + (long long)req * p.table_stride;
+
+        // the two rows of this thread: last key each attends to
+        int lim[2];
+        long long q_off[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int row = row0 + min(g + 8 * e, rows - 1);
+            const int tok = row / p.group, head = kvh * p.group + (row - tok * p.group);
+            lim[e] = p.causal ? min(r.len, r.len - r.q + tok + 1) - 1 : r.len - 1;
+            q_off[e] = (long long)(r.first + tok) * p.q_tok + (long long)head * p.q_head;
+        }
+        const int tok_first = row0 / p.group, tok_last = (row0 + rows - 1) / p.group;
+        const int lim_first = p.causal ? r.len - r.q + tok_first : r.len - 1;   // smallest limit of the tile
+        const int keys = p.causal ? max(0, r.len - r.q + tok_last + 1) : r.len;
+        uint32_t qa[D / 16][4];
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                qa[k][e] = *reinterpret_cast<const uint32_t*>(p.q + q_off[e] + k * 16 + t4 * 2);
+                qa[k][2 + e] = *reinterpret_cast<const uint32_t*>(p.q + q_off[e] + k * 16 + 8 + t4 * 2);
+            }
+        }
+
+        State<D> st;
+        st.m[0] = st.m[1] = -INFINITY;
+        st.l[0] = st.l[1] = 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y) st.acc[x][y] = 0.f;
+
+        for (int key0 = warp * kKeys; key0 < keys; key0 += kWarps * kKeys) {
+            // ---- load: page sizes are multiples of 8, so 8 keys share a page
+            bool bad = false;
+            long long kb[2], vb[2];
+            bool ok[2];
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int key = key0 + 8 * hf;
+                ok[hf] = key < r.len;
+                const int pi = page_index(key, p.page_size, p.page_shift);
+                const int page = ok[hf] ? table[pi] : 0;
+                if (!page_ok(page, p.num_pages)) {
+                    ok[hf] = false;
+                    bad = true;
+                }
+                const int off = key - pi * p.page_size;
+                kb[hf] = ok[hf] ? row_offset(p.lk, page, off, kvh) : 0;
+                vb[hf] = ok[hf] ? row_offset(p.lv, page, off, kvh) : 0;
+            }
+            if (bad && lane == 0) atomicOr(p.status, kStatusBadPage);
+            constexpr int kPieces = D / 8;                   // 16-byte pieces of a row
+            constexpr int kRowsPerOp = 32 / kPieces;
+            __syncwarp();
+#pragma unroll
+            for (int x = 0; x < kKeys / kRowsPerOp; ++x) {
+                const int row = x * kRowsPerOp + lane / kPieces, piece = lane % kPieces;
+                const int hf = row >> 3, in = row & 7;
+                const bool take = ok[hf] && key0 + row < r.len;
+                const uint32_t dst = (uint32_t)(row * D * 2 + ((piece ^ in) << 4));
+                cp_async16(sK + dst, p.kc + kb[hf] + (take ? in * p.lk.st : 0) + piece * 8, take);
+                cp_async16(sV + dst, p.vc + vb[hf] + (take ? in * p.lv.st : 0) + piece * 8, take);
+            }
+            cp_async_commit();
+            cp_async_wait<0>();
+            __syncwarp();
+
+            // ---- S = Q K^T: 16 rows x 16 keys
+            float s[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+                // matrices: keys 0-7 | 8-15, columns 16k..16k+7 | 16k+8..
+                const int row = (lane & 7) + ((lane >> 4) << 3), piece = 2 * k + ((lane >> 3) & 1);
+                uint32_t b[4];
+                ldmatrix4(b, sK + row * D * 2 + ((piece ^ (row & 7)) << 4));
+                Op::mma(s[0], qa[k], b[0], b[1]);
+                Op::mma(s[1], qa[k], b[2], b[3]);
+            }
+
+            // ---- softmax
+            const bool masked = key0 + kKeys - 1 > lim_first || key0 + kKeys > r.len;
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) {
+                    s[x][y] *= p.scale_log2;
+                    if (masked && key0 + 8 * x + 2 * t4 + (y & 1) > lim[y >> 1]) s[x][y] = -INFINITY;
+                }
+            float alpha[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = max_nan(max_nan(s[0][2 * e], s[0][2 * e + 1]), max_nan(s[1][2 * e], s[1][2 * e + 1]));
+                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float m = max_nan(st.m[e], mx);
+                alpha[e] = m == -INFINITY ? 1.f : ex2_approx(st.m[e] - m);
+                st.m[e] = m;
+                const float ref = m == -INFINITY ? 0.f : m - Op::kShift;
+                float sum = 0.f;
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float w = ex2_approx(s[x][2 * e + y] - ref);
+                        s[x][2 * e + y] = w;
+                        sum += w;
+                    }
+                st.l[e] = st.l[e] * alpha[e] + sum;
+            }
+            if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) st.acc[x][y] *= alpha[y >> 1];
+            }
+            // Weights rounded to the operand type (half a step of 2^-9 or
+            // 2^-12 each); l sums them unrounded.
+            uint32_t pa[4];
+            pa[0] = Op::pack(s[0][0], s[0][1]);
+            pa[1] = Op::pack(s[0][2], s[0][3]);
+            pa[2] = Op::pack(s[1][0], s[1][1]);
+            pa[3] = Op::pack(s[1][2], s[1][3]);
+
+            // ---- O += P V
+            bool odd = false;
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+                // matrices: keys 0-7 | 8-15 of columns 16x.., then of 16x + 8..
+                const int row = lane & 15, piece = 2 * x + (lane >> 4);
+                uint32_t b[4];
+                ldmatrix4_trans(b, sV + row * D * 2 + ((piece ^ (row & 7)) << 4));
+                if (!masked) {
+                    Op::mma(st.acc[2 * x], pa, b[0], b[1]);
+                    Op::mma(st.acc[2 * x + 1], pa, b[2], b[3]);
+                } else {
+                    odd |= Op::nonfinite(b[0]) || Op::nonfinite(b[1]) || Op::nonfinite(b[2]) || Op::nonfinite(b[3]);
+                }
+            }
+            if (masked) {
+                // A weight of 0 does not hide an infinity or a NaN in V, so
+                // where rows see different keys and V holds one, the keys are
+                // added one by one to the rows that see them.
+                if (!__any_sync(0xffffffffu, odd)) {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const int row = lane & 15, piece = 2 * x + (lane >> 4);
+                        uint32_t b[4];
+                        ldmatrix4_trans(b, sV + row * D * 2 + ((piece ^ (row & 7)) << 4));
+                        Op::mma(st.acc[2 * x], pa, b[0], b[1]);
+                        Op::mma(st.acc[2 * x + 1], pa, b[2], b[3]);
+                    }
+                } else {
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        const int row = lane & 15, piece = 2 * x + (lane >> 4);
+                        uint32_t b[4];
+                        ldmatrix4_trans(b, sV + row * D * 2 + ((piece ^ (row & 7)) << 4));
+#pragma unroll 1
+                        for (int key = 0; key < kKeys; ++key) {
+                            const uint32_t sel = ((key & 7) >> 1) == t4 ? (key & 1 ? 0xffff0000u : 0x0000ffffu) : 0u;
+                            const uint32_t lo = key < 8 ? sel : 0u, hi = key < 8 ? 0u : sel;
+                            const uint32_t a[4] = {pa[0] & lo, pa[1] & lo, pa[2] & hi, pa[3] & hi};
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                Op::mma(d, a, b[2 * y] & lo, b[2 * y + 1] & hi);
+#pragma unroll
+                                for (int z = 0; z < 4; ++z)
+                                    if (key0 + key <= lim[z >> 1]) st.acc[2 * x + y][z] += d[z];
+                            }
+                        }
+                    }
+                }
+            }
+        }
+
+        // ---- merge the eight warps
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 1);
+            st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 2);
+        }
+        __syncwarp();
+        float* mo = reinterpret_cast<float*>(my);
+#pragma unroll
+        for (int x = 0; x < D / 8; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+                *reinterpret_cast<float2*>(mo + (g + 8 * e) * D + 8 * x + 2 * t4) =
+                    make_float2(st.acc[x][2 * e], st.acc[x][2 * e + 1]);
+        if (t4 == 0) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                mo[kRows * D + g + 8 * e] = st.m[e];
+                mo[kRows * D + kRows + g + 8 * e] = st.l[e];
+            }
+        }
+        __syncthreads();
+        constexpr int kPer = kRows * D / kThreads;       // columns of a thread
+        const int row = tid / (D / kPer), col = tid % (D / kPer) * kPer;
+        if (row < rows) {
+            auto part = [&](int w) { return reinterpret_cast<const float*>(smem_raw + w * C::kWarpBytes); };
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) m = max_nan(m, part(w)[kRows * D + row]);
+            float l = 0.f, out[kPer];
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) out[c] = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float mw = part(w)[kRows * D + row];
+                if (mw == -INFINITY) continue;           // no key of this row
+                const float f = ex2_approx(mw - m);
+                l += f * part(w)[kRows * D + kRows + row];
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) out[c] += f * part(w)[row * D + col + c];
+            }
+            const float inv = m == -INFINITY ? 0.f : 1.f / l;
+            const int pr = row0 + row, tok = pr / p.group, head = kvh * p.group + (pr - tok * p.group);
+            uint16_t* dst = p.o + (long long)(r.first + tok) * p.o_tok + (long long)head * p.o_head + col;
+            uint32_t pk[kPer / 2];
+#pragma unroll
+            for (int c = 0; c < kPer / 2; ++c) pk[c] = Op::pack(out[2 * c] * inv, out[2 * c + 1] * inv);
+            if constexpr (kPer == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+            if (col == 0)
+                p.lse[(long long)head * p.tokens + r.first + tok] =
+                    m == -INFINITY ? -INFINITY : (m - Op::kShift + log2f(l)) * 0.69314718055994531f;
+        }
+    }
+}
+
+}  // namespace rows
+}  // namespace paged
+}  // namespace ra

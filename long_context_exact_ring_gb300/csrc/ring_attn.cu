@@ -4,7 +4,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
+#include <climits>
 #include <cmath>
 #include <cstdio>
 #include <cstring>
@@ -15,6 +17,7 @@
 #include "fwd_kernel.cuh"
 #include "bwd_kernel.cuh"
 #include "small_kernels.cuh"
+#include "paged_attn.cuh"
 
 namespace {
 
@@ -260,6 +263,7 @@ const char* ring_attn_status_string(int status)
     case RA_ERR_UNSUPPORTED: return "RA_ERR_UNSUPPORTED";
     case RA_ERR_CUDA: return "RA_ERR_CUDA";
     case RA_ERR_DEVICE_TIMEOUT: return "RA_ERR_DEVICE_TIMEOUT";
+    case RA_ERR_BAD_PAGE: return "RA_ERR_BAD_PAGE";
     default: return "RA_UNKNOWN_STATUS";
     }
 }
@@ -944,7 +948,10 @@ int ring_attn_check_status(void* stream)
     if (e == cudaSuccess) e = cudaMemsetAsync(st->status, 0, sizeof(uint32_t), s);
     if (e == cudaSuccess) e = cudaStreamSynchronize(s);
     if (e != cudaSuccess) return fail_cuda(e, "status read");
-    return word ? RA_ERR_DEVICE_TIMEOUT : RA_OK;
+    if (word & ~(uint32_t)ra::kStatusBadPage) return RA_ERR_DEVICE_TIMEOUT;
+    return word ? RA_ERR_BAD_PAGE : RA_OK;
 }
 
 }  // extern "C"
+
+#include "paged_abi.cuh"

@@ -20,6 +20,7 @@ namespace ra {
 enum : uint32_t {
     kStatusTimeout = 1u,   // a bounded wait ran out
     kStatusAborted = 2u,   // a CTA left early because another role timed out
+    kStatusBadPage = 4u,   // a page or slot outside its pool was met and not followed
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p)
