@@ -513,7 +513,7 @@ int ring_attn_trace_visits(int *buf, long long capacity);
  * for the kernel named (one of "ring_fwd_kernel", "ring_bwd_kernel",
  * "bwd_prep_kernel", "dq_convert_kernel", "merge_partials_kernel",
  * "f32_to_bf16_kernel", "paged_plan_kernel", "paged_append_kernel",
- * "paged_rows_kernel"), the
+ * "paged_rows_kernel", "paged_join_kernel"), the
  * number of launches and their summed device time in milliseconds since
  * the last ring_attn_profile_reset.  Host-side state, process-wide; not for
  * use inside CUDA graph capture.  RA_ERR_INVALID_ARG for an unknown name.

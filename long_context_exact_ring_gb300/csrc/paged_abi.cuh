@@ -136,7 +136,7 @@ int paged_kv_append(const void* k, const long long* k_strides, const void* v, co
 size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d)
 {
     if (n <= 0 || tokens <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
-    return 256;
+    return (ra::paged::rows::workspace_bytes(d) + 255) / 256 * 256;
 }
 
 int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cache, const long long* k_cache_strides,
@@ -201,21 +201,30 @@ int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cach
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.status = st->status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    auto launch = [&](auto kernel, int smem) {
+    namespace pr = ra::paged::rows;
+    const pr::Workspace ws = pr::workspace(workspace);
+    const int blocks = std::min(st->num_sms, pr::kMaxBlocks);
+    auto launch = [&](auto kernel, auto join, int smem) {
         const int e = allow_smem(kernel, smem);
         if (e != RA_OK) return e;
-        ra::prof::Scope ps(ra::prof::kPagedRows, s);
-        kernel<<<st->num_sms, ra::paged::rows::kThreads, smem, s>>>(p);
+        {
+            ra::prof::Scope ps(ra::prof::kPagedRows, s);
+            kernel<<<blocks, pr::kThreads, smem, s>>>(p, ws);
+            ps.done();
+        }
+        ra::prof::Scope ps(ra::prof::kPagedJoin, s);
+        join<<<blocks, pr::kThreads, 0, s>>>(p, ws, blocks);
         ps.done();
         const cudaError_t ce = cudaGetLastError();
-        return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged_rows_kernel launch");
+        return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged attention launch");
     };
-    namespace pr = ra::paged::rows;
     if (d == 128)
-        return dtype == RA_FP16 ? launch(pr::paged_rows_kernel<128, true>, pr::Cfg<128>::kSmemBytes)
-                                : launch(pr::paged_rows_kernel<128, false>, pr::Cfg<128>::kSmemBytes);
-    return dtype == RA_FP16 ? launch(pr::paged_rows_kernel<64, true>, pr::Cfg<64>::kSmemBytes)
-                            : launch(pr::paged_rows_kernel<64, false>, pr::Cfg<64>::kSmemBytes);
+        return dtype == RA_FP16
+                   ? launch(pr::paged_rows_kernel<128, true>, pr::paged_join_kernel<128, true>, pr::Cfg<128>::kSmemBytes)
+                   : launch(pr::paged_rows_kernel<128, false>, pr::paged_join_kernel<128, false>, pr::Cfg<128>::kSmemBytes);
+    return dtype == RA_FP16
+               ? launch(pr::paged_rows_kernel<64, true>, pr::paged_join_kernel<64, true>, pr::Cfg<64>::kSmemBytes)
+               : launch(pr::paged_rows_kernel<64, false>, pr::paged_join_kernel<64, false>, pr::Cfg<64>::kSmemBytes);
 }
 
 }  // extern "C"

@@ -122,14 +122,47 @@ constexpr int kRows = 16;        // packed rows of a tile: one m16n8k16 operand
 constexpr int kKeys = 16;        // keys of a warp's step
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = kKeys * kWarps;   // keys of a block's step, and of the smallest piece of work
+constexpr int kMaxBlocks = 256;
 
 template <int D>
 struct Cfg {
     static constexpr int kChunkBytes = kKeys * D * 2;              // a warp's K (or V) of one step
-    static constexpr int kMergeBytes = kRows * D * 4 + 2 * kRows * 4;
-    static constexpr int kWarpBytes = 2 * kChunkBytes > kMergeBytes ? 2 * kChunkBytes : (kMergeBytes + 127) / 128 * 128;
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kWarpBytes = 2 * kChunkBytes * kStages;
     static constexpr int kSmemBytes = kWarps * kWarpBytes;
+    static_assert(kWarpBytes >= kRows * D * 4 + 2 * kRows * 4, "a warp's state fits over its stages");
 };
+
+// A tile's keys are cut where one block's share of the work ends and the
+// next one's begins, so a block has at most two unfinished tiles: one that
+// it takes over from the block before (part 0) and one that it leaves to
+// the block behind (part 1).
+struct PartInfo {
+    int req;        // -1: no such part
+    int kvh, row0;
+    int last;       // part 0 only: its tile ends in this block
+};
+
+struct Workspace {
+    PartInfo* info;   // [blocks][2]
+    float* ml;        // [blocks][2][2][kRows] reference and sum of the exponentials
+    float* acc;       // [blocks][2][kRows][D] sums, not normalized
+};
+
+__host__ __device__ inline size_t workspace_bytes(int D)
+{
+    return (size_t)kMaxBlocks * 2 * (sizeof(PartInfo) + (2 * kRows + (size_t)kRows * D) * 4);
+}
+
+__host__ __device__ inline Workspace workspace(void* base)
+{
+    Workspace w;
+    w.info = static_cast<PartInfo*>(base);
+    w.ml = reinterpret_cast<float*>(w.info + 2 * kMaxBlocks);
+    w.acc = w.ml + (size_t)kMaxBlocks * 2 * 2 * kRows;
+    return w;
+}
 
 // One warp's running state of a tile: 16 rows, of which a thread holds two.
 template <int D>
@@ -138,48 +171,84 @@ struct State {
     float acc[D / 8][4];
 };
 
-// One block per (request, key/value head, tile of 16 packed rows), taken in
-// turn.  Every warp streams its own 16 keys out of each 128 through its own
-// corner of shared memory, with no barrier between warps, and keeps its own
-// softmax state; the states of the eight warps are merged at the end.
+// Writes kPer columns of a finished row.
+template <int kPer, bool kHalf>
+__device__ __forceinline__ void store_row(const AttnParams& p, const Request& r, int kvh, int packed, int col,
+                                          const float (&out)[kPer], float m, float l)
+{
+    using Op = Operand<kHalf>;
+    // no key, or none with a weight: O = 0, LSE = -inf
+    const float inv = m == -INFINITY ? 0.f : 1.f / l;
+    const int tok = packed / p.group, head = kvh * p.group + (packed - tok * p.group);
+    uint16_t* dst = p.o + (long long)(r.first + tok) * p.o_tok + (long long)head * p.o_head + col;
+    uint32_t pk[kPer / 2];
+#pragma unroll
+    for (int c = 0; c < kPer / 2; ++c) pk[c] = Op::pack(out[2 * c] * inv, out[2 * c + 1] * inv);
+    if constexpr (kPer == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+    else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+    if (col == 0)
+        p.lse[(long long)head * p.tokens + r.first + tok] =
+            m == -INFINITY ? -INFINITY : (m - Op::kShift + log2f(l)) * 0.69314718055994531f;
+}
+
+// The work is the list of (request, key/value head, tile of 16 packed rows,
+// 128 keys); every block takes an equal, contiguous share of it, so a single
+// long context keeps all SMs reading as well as many short ones do.  Every
+// warp streams its own 16 keys out of each 128 through its own ring of
+// stages (asynchronous copies, no barrier between warps) and keeps its own
+// softmax state; the states of the eight warps are merged at the end of a
+// tile, or of the block's part of it, and parts by paged_join_kernel.
+//
+// Bound by HBM: K and V are read once per 16 packed rows.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParams p)
+__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParams p, const Workspace ws)
 {
     using C = Cfg<D>;
     using Op = Operand<kHalf>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ long long s_scratch[kWarps + 1];
-    __shared__ int s_item[2];
+    __shared__ long long s_offset;
+    __shared__ int s_req;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int g = lane >> 2, t4 = lane & 3;
     uint8_t* my = smem_raw + warp * C::kWarpBytes;
-    const uint32_t sK = smem_u32(my), sV = sK + C::kChunkBytes;
+    const uint32_t s_my = smem_u32(my);
 
-    // tiles of all requests before each thread's share of them
+    // ---- this block's share of the work
+    auto tiles_of = [&](const Request& r) { return (r.q * p.group + kRows - 1) / kRows; };
+    auto units_of = [&](const Request& r) { return max(1, (r.len + kUnit - 1) / kUnit); };
+    auto work_of = [&](int i) {
+        const Request r = load_request(p, i);
+        return (long long)tiles_of(r) * p.kv_heads * units_of(r);
+    };
     const int per = (p.n + kThreads - 1) / kThreads;
     const int i0 = min(p.n, tid * per), i1 = min(p.n, i0 + per);
-    auto tiles_of = [&](int i) {
-        const Request r = load_request(p, i);
-        return ((long long)r.q * p.group + kRows - 1) / kRows * p.kv_heads;
-    };
     long long mine = 0, total;
-    for (int i = i0; i < i1; ++i) mine += tiles_of(i);
+    for (int i = i0; i < i1; ++i) mine += work_of(i);
     const long long before = block_exclusive_sum(mine, s_scratch, &total);
+    const int G = gridDim.x, b = blockIdx.x;
+    long long left = total / G + (b < total % G);                    // units of this block
+    const long long start = total / G * b + min((long long)b, total % G);
+    if (tid < 2) ws.info[2 * b + tid].req = -1;
+    if (left == 0) return;
+    if (before <= start && start < before + mine) {
+        long long x = start - before;
+        int i = i0;
+        for (long long c; x >= (c = work_of(i)); ++i) x -= c;
+        s_req = i;
+        s_offset = x;
+    }
+    __syncthreads();
+    int req = s_req;
+    long long offset = s_offset;                                     // units into the request
 
-    for (long long item = blockIdx.x; item < total; item += gridDim.x) {
-        __syncthreads();
-        if (before <= item && item < before + mine) {
-            long long x = item - before;
-            int i = i0;
-            for (long long c; x >= (c = tiles_of(i)); ++i) x -= c;
-            s_item[0] = i;
-            s_item[1] = (int)x;
-        }
-        __syncthreads();
-        const int req = s_item[0];
+    while (true) {
         const Request r = load_request(p, req);
-        const int tiles = (r.q * p.group + kRows - 1) / kRows;
-        const int kvh = s_item[1] / tiles, row0 = (s_item[1] - kvh * tiles) * kRows;
+        const int tiles = tiles_of(r), units = units_of(r);
+        const int item = (int)(offset / units);
+        const int u0 = (int)(offset - (long long)item * units);
+        const int u1 = (int)min((long long)units, u0 + left);
+        const int kvh = item / tiles, row0 = (item - kvh * tiles) * kRows;
         const int rows = min(kRows, r.q * p.group - row0);
         const int* table = p.table + (long long)req * p.table_stride;
 
@@ -195,7 +264,55 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
         }
         const int tok_first = row0 / p.group, tok_last = (row0 + rows - 1) / p.group;
         const int lim_first = p.causal ? r.len - r.q + tok_first : r.len - 1;   // smallest limit of the tile
-        const int keys = p.causal ? max(0, r.len - r.q + tok_last + 1) : r.len;
+        const int keys = min(u1 * kUnit, p.causal ? r.len - r.q + tok_last + 1 : r.len);
+
+        // ---- copies: page sizes are multiples of 8, so 8 keys share a page;
+        // the page numbers are fetched one step ahead of the copies
+        constexpr int kPieces = D / 8;                   // 16-byte pieces of a row
+        constexpr int kRowsPerOp = 32 / kPieces;
+        auto fetch_pages = [&](int key0, int (&pg)[2]) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
+                pg[hf] = key0 + 8 * hf < keys ? table[page_index(key0 + 8 * hf, p.page_size, p.page_shift)] : 0;
+        };
+        auto copy = [&](int key0, int stage, const int (&pg)[2]) {
+            long long kb[2], vb[2];
+            bool ok[2], bad = false;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const int key = key0 + 8 * hf;
+                ok[hf] = key < keys;
+                if (!page_ok(pg[hf], p.num_pages)) {
+                    ok[hf] = false;
+                    bad = true;
+                }
+                const int off = key - page_index(key, p.page_size, p.page_shift) * p.page_size;
+                kb[hf] = ok[hf] ? row_offset(p.lk, pg[hf], off, kvh) : 0;
+                vb[hf] = ok[hf] ? row_offset(p.lv, pg[hf], off, kvh) : 0;
+            }
+            if (bad && lane == 0) atomicOr(p.status, kStatusBadPage);
+            const uint32_t sK = s_my + stage * 2 * C::kChunkBytes, sV = sK + C::kChunkBytes;
+#pragma unroll
+            for (int x = 0; x < kKeys / kRowsPerOp; ++x) {
+                const int row = x * kRowsPerOp + lane / kPieces, piece = lane % kPieces;
+                const int hf = row >> 3, in = row & 7;
+                const bool take = ok[hf] && key0 + row < r.len;
+                const uint32_t dst = (uint32_t)(row * D * 2 + ((piece ^ in) << 4));
+                cp_async16(sK + dst, p.kc + kb[hf] + (take ? in * p.lk.st : 0) + piece * 8, take);
+                cp_async16(sV + dst, p.vc + vb[hf] + (take ? in * p.lv.st : 0) + piece * 8, take);
+            }
+        };
+        const int first = u0 * kUnit + warp * kKeys;
+        int pg[2];
+        fetch_pages(first, pg);
+#pragma unroll
+        for (int x = 0; x < C::kStages - 1; ++x) {
+            const int key0 = first + x * kUnit;
+            if (key0 < keys) copy(key0, x, pg);
+            cp_async_commit();
+            fetch_pages(key0 + kUnit, pg);
+        }
+
         uint32_t qa[D / 16][4];
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
@@ -214,41 +331,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
 #pragma unroll
             for (int y = 0; y < 4; ++y) st.acc[x][y] = 0.f;
 
-        for (int key0 = warp * kKeys; key0 < keys; key0 += kWarps * kKeys) {
-            // ---- load: page sizes are multiples of 8, so 8 keys share a page
-            bool bad = false;
-            long long kb[2], vb[2];
-            bool ok[2];
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int key = key0 + 8 * hf;
-                ok[hf] = key < r.len;
-                const int pi = page_index(key, p.page_size, p.page_shift);
-                const int page = ok[hf] ? table[pi] : 0;
-                if (!page_ok(page, p.num_pages)) {
-                    ok[hf] = false;
-                    bad = true;
-                }
-                const int off = key - pi * p.page_size;
-                kb[hf] = ok[hf] ? row_offset(p.lk, page, off, kvh) : 0;
-                vb[hf] = ok[hf] ? row_offset(p.lv, page, off, kvh) : 0;
+        int stage = 0;
+        for (int key0 = first; key0 < keys; key0 += kUnit) {
+            {
+                const int ahead = key0 + (C::kStages - 1) * kUnit;
+                if (ahead < keys) copy(ahead, stage == 0 ? C::kStages - 1 : stage - 1, pg);
+                cp_async_commit();
+                fetch_pages(ahead + kUnit, pg);
             }
-            if (bad && lane == 0) atomicOr(p.status, kStatusBadPage);
-            constexpr int kPieces = D / 8;                   // 16-byte pieces of a row
-            constexpr int kRowsPerOp = 32 / kPieces;
+            cp_async_wait<C::kStages - 1>();
             __syncwarp();
-#pragma unroll
-            for (int x = 0; x < kKeys / kRowsPerOp; ++x) {
-                const int row = x * kRowsPerOp + lane / kPieces, piece = lane % kPieces;
-                const int hf = row >> 3, in = row & 7;
-                const bool take = ok[hf] && key0 + row < r.len;
-                const uint32_t dst = (uint32_t)(row * D * 2 + ((piece ^ in) << 4));
-                cp_async16(sK + dst, p.kc + kb[hf] + (take ? in * p.lk.st : 0) + piece * 8, take);
-                cp_async16(sV + dst, p.vc + vb[hf] + (take ? in * p.lv.st : 0) + piece * 8, take);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            __syncwarp();
+            const uint32_t sK = s_my + stage * 2 * C::kChunkBytes, sV = sK + C::kChunkBytes;
+            stage = stage + 1 == C::kStages ? 0 : stage + 1;
 
             // ---- S = Q K^T: 16 rows x 16 keys
             float s[2][4];
@@ -267,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
             }
 
             // ---- softmax
-            const bool masked = key0 + kKeys - 1 > lim_first || key0 + kKeys > r.len;
+            const bool masked = key0 + kKeys - 1 > lim_first;
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -361,9 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
                     }
                 }
             }
+            __syncwarp();     // the stage may be written again
         }
 
         // ---- merge the eight warps
+        cp_async_wait<0>();
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 1);
@@ -387,36 +483,86 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
         __syncthreads();
         constexpr int kPer = kRows * D / kThreads;       // columns of a thread
         const int row = tid / (D / kPer), col = tid % (D / kPer) * kPer;
-        if (row < rows) {
-            auto part = [&](int w) { return reinterpret_cast<const float*>(smem_raw + w * C::kWarpBytes); };
-            float m = -INFINITY;
+        auto part = [&](int w) { return reinterpret_cast<const float*>(smem_raw + w * C::kWarpBytes); };
+        float m = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m = max_nan(m, part(w)[kRows * D + row]);
-            float l = 0.f, out[kPer];
+        for (int w = 0; w < kWarps; ++w) m = max_nan(m, part(w)[kRows * D + row]);
+        float l = 0.f, out[kPer];
 #pragma unroll
-            for (int c = 0; c < kPer; ++c) out[c] = 0.f;
+        for (int c = 0; c < kPer; ++c) out[c] = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float mw = part(w)[kRows * D + row];
-                if (mw == -INFINITY) continue;           // no key of this row
-                const float f = ex2_approx(mw - m);
-                l += f * part(w)[kRows * D + kRows + row];
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = part(w)[kRows * D + row];
+            if (mw == -INFINITY) continue;           // no key of this row
+            const float f = ex2_approx(mw - m);
+            l += f * part(w)[kRows * D + kRows + row];
 #pragma unroll
-                for (int c = 0; c < kPer; ++c) out[c] += f * part(w)[row * D + col + c];
-            }
-            const float inv = m == -INFINITY ? 0.f : 1.f / l;
-            const int pr = row0 + row, tok = pr / p.group, head = kvh * p.group + (pr - tok * p.group);
-            uint16_t* dst = p.o + (long long)(r.first + tok) * p.o_tok + (long long)head * p.o_head + col;
-            uint32_t pk[kPer / 2];
-#pragma unroll
-            for (int c = 0; c < kPer / 2; ++c) pk[c] = Op::pack(out[2 * c] * inv, out[2 * c + 1] * inv);
-            if constexpr (kPer == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
-            if (col == 0)
-                p.lse[(long long)head * p.tokens + r.first + tok] =
-                    m == -INFINITY ? -INFINITY : (m - Op::kShift + log2f(l)) * 0.69314718055994531f;
+            for (int c = 0; c < kPer; ++c) out[c] += f * part(w)[row * D + col + c];
         }
+        if (u0 == 0 && u1 == units) {
+            if (row < rows) store_row<kPer, kHalf>(p, r, kvh, row0 + row, col, out, m, l);
+        } else {
+            const int slot = 2 * b + (u0 == 0);
+            float* dst = ws.acc + ((size_t)slot * kRows + row) * D + col;
+#pragma unroll
+            for (int c = 0; c < kPer; c += 4)
+                *reinterpret_cast<float4*>(dst + c) = make_float4(out[c], out[c + 1], out[c + 2], out[c + 3]);
+            if (col == 0) {
+                ws.ml[slot * 2 * kRows + row] = m;
+                ws.ml[slot * 2 * kRows + kRows + row] = l;
+            }
+            if (tid == 0) ws.info[slot] = PartInfo{req, kvh, row0, u1 == units};
+        }
+        left -= u1 - u0;
+        if (left == 0) break;
+        offset += u1 - u0;
+        if (offset == (long long)tiles * p.kv_heads * units) {
+            offset = 0;
+            do ++req;
+            while (work_of(req) == 0);       // some later request has the work that is left
+        }
+        __syncthreads();                     // the states are read before the stages are filled again
     }
+}
+
+// Joins the parts of a tile that several blocks had a share of: the block
+// that began it, then those behind it, in order -- the sum does not depend
+// on which finished first.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kThreads) paged_join_kernel(const AttnParams p, const Workspace ws, int blocks)
+{
+    const int b = blockIdx.x;
+    const PartInfo info = ws.info[2 * b + 1];
+    if (info.req < 0) return;
+    constexpr int kPer = kRows * D / kThreads;
+    const int row = threadIdx.x / (D / kPer), col = threadIdx.x % (D / kPer) * kPer;
+    float m = -INFINITY, l = 0.f, out[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) out[c] = 0.f;
+    for (int x = b; x < blocks; ++x) {
+        const int slot = x == b ? 2 * b + 1 : 2 * x;
+        bool last = false;
+        if (x != b) {
+            const PartInfo next = ws.info[slot];
+            if (next.req < 0) continue;      // a block without work
+            last = next.last;
+        }
+        const float mx = ws.ml[slot * 2 * kRows + row], lx = ws.ml[slot * 2 * kRows + kRows + row];
+        const float* src = ws.acc + ((size_t)slot * kRows + row) * D + col;
+        float v[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; c += 4) *reinterpret_cast<float4*>(v + c) = *reinterpret_cast<const float4*>(src + c);
+        if (mx != -INFINITY) {
+            const float to = max_nan(m, mx), fa = ex2_approx(m - to), fb = ex2_approx(mx - to);
+            m = to;
+            l = l * fa + lx * fb;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) out[c] = out[c] * fa + v[c] * fb;
+        }
+        if (last) break;
+    }
+    const Request r = load_request(p, info.req);
+    if (info.row0 + row < r.q * p.group) store_row<kPer, kHalf>(p, r, info.kvh, info.row0 + row, col, out, m, l);
 }
 
 }  // namespace rows
