@@ -378,8 +378,7 @@ typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
  * seq_lens_out may be seq_lens and counts_out may be counts (a loop's state,
  * updated in place); otherwise buffers do not overlap.  Where they are not
  * updated in place the call can be repeated with the same result.
- * n * max_pages and num_pages are at most 2^30, max_pages * page_size below
- * 2^31.
+ * n * max_pages, num_pages and max_pages * page_size are at most 2^30.
  */
 int paged_kv_plan(const int *seq_lens, const int *new_lens, int n, int *block_table,
                   long long table_stride, int max_pages, int *free_list, int num_pages,
@@ -426,6 +425,7 @@ size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d);
  *   max_q        an upper bound of the new tokens of one request, for the
  *                choice of kernels only: results do not depend on it.
  *   dtype        RA_BF16 or RA_FP16, of q, the pools and o.
+ *   max_pages    as in paged_kv_plan: max_pages * page_size at most 2^30.
  *   H / H_kv     a whole number up to 128 (more: RA_ERR_UNSUPPORTED).
  *   workspace    paged_attn_workspace_size bytes, 256-byte aligned, of any
  *                contents; calls that may run at the same time need one each.
@@ -513,7 +513,8 @@ int ring_attn_trace_visits(int *buf, long long capacity);
  * for the kernel named (one of "ring_fwd_kernel", "ring_bwd_kernel",
  * "bwd_prep_kernel", "dq_convert_kernel", "merge_partials_kernel",
  * "f32_to_bf16_kernel", "paged_plan_kernel", "paged_append_kernel",
- * "paged_rows_kernel", "paged_join_kernel"), the
+ * "paged_rows_kernel", "paged_join_kernel",
+ * "paged_tiles_kernel"), the
  * number of launches and their summed device time in milliseconds since
  * the last ring_attn_profile_reset.  Host-side state, process-wide; not for
  * use inside CUDA graph capture.  RA_ERR_INVALID_ARG for an unknown name.

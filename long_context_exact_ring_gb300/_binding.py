@@ -492,7 +492,7 @@ def trace_visits(buf=None) -> None:
 
 KERNELS = ("ring_fwd_kernel", "ring_bwd_kernel", "bwd_prep_kernel", "dq_convert_kernel",
            "merge_partials_kernel", "f32_to_bf16_kernel", "paged_plan_kernel", "paged_append_kernel",
-           "paged_rows_kernel", "paged_join_kernel")
+           "paged_rows_kernel", "paged_join_kernel", "paged_tiles_kernel")
 
 
 def profile_enable(on: bool = True) -> None:

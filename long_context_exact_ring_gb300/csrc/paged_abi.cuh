@@ -57,6 +57,107 @@ int allow_smem(Kernel kernel, int bytes)
     return e == cudaSuccess ? RA_OK : fail_cuda(e, "cudaFuncSetAttribute");
 }
 
+// 4-D tiled map of 2-byte elements with 128-byte swizzle, 64 columns wide.
+// Strides in elements; that of an extent-1 dimension is never stepped along
+// and is replaced by a valid one.
+int make_paged_map(CUtensorMap* map, const void* ptr, bool half, int d, const int (&extents)[3],
+                   const long long (&strides)[3], const int (&box_rows)[3])
+{
+    cuuint64_t dims[4] = {(cuuint64_t)d, 1, 1, 1}, st[3];
+    cuuint32_t box[4] = {64u, 1u, 1u, 1u}, estr[4] = {1u, 1u, 1u, 1u};
+    for (int x = 0; x < 3; ++x) {
+        dims[x + 1] = (cuuint64_t)extents[x];
+        st[x] = (cuuint64_t)(extents[x] > 1 ? strides[x] : d) * 2;
+        box[x + 1] = (cuuint32_t)box_rows[x];
+    }
+    const CUresult r = g_encode(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                                const_cast<void*>(ptr), dims, st, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) {
+        std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled (paged) failed (%d)", (int)r);
+        return RA_ERR_CUDA;
+    }
+    return RA_OK;
+}
+
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Up to 16 packed rows (new tokens x query heads of a key/value head) a
+// request is served by paged_rows_kernel, above by paged_tiles_kernel.
+constexpr int kFewRows = 16;
+
+template <int D, bool kHalf>
+int launch_rows(const ra::paged::AttnParams& p, void* workspace, ra::paged::RowRange range, int blocks, cudaStream_t s)
+{
+    namespace pr = ra::paged::rows;
+    const int e = allow_smem(pr::paged_rows_kernel<D, kHalf>, pr::Cfg<D>::kSmemBytes);
+    if (e != RA_OK) return e;
+    const ra::paged::Workspace ws = ra::paged::workspace(workspace, pr::kRows);
+    {
+        ra::prof::Scope ps(ra::prof::kPagedRows, s);
+        pr::paged_rows_kernel<D, kHalf><<<blocks, pr::kThreads, pr::Cfg<D>::kSmemBytes, s>>>(p, ws, range);
+        ps.done();
+    }
+    ra::prof::Scope ps(ra::prof::kPagedJoin, s);
+    ra::paged::paged_join_kernel<D, kHalf, pr::kRows, pr::kRows><<<blocks, 256, 0, s>>>(
+        p, ws, blocks, pr::kRows, ra::paged::Operand<kHalf>::kShift);
+    ps.done();
+    const cudaError_t ce = cudaGetLastError();
+    return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged_rows_kernel launch");
+}
+
+template <int D, bool kHalf>
+int launch_tiles(const ra::paged::AttnParams& p, void* workspace, ra::paged::RowRange range, int blocks,
+                 cudaStream_t s)
+{
+    namespace pt = ra::paged::tiles;
+    const int e = allow_smem(pt::paged_tiles_kernel<D, kHalf>, pt::Cfg<D>::kSmemBytes);
+    if (e != RA_OK) return e;
+    pt::TileParams tp;
+    tp.a = p;
+    tp.ws = ra::paged::workspace(workspace, pt::kTileRows);
+    tp.range = range;
+    tp.tok_tile = pt::kBM / p.group;
+    tp.box_rows = std::min(p.page_size & -p.page_size, pt::kBN);
+    tp.wait_limit_ns = g_wait_limit_ns.load();
+    CUtensorMap mq, mk, mv;
+    int rc = make_paged_map(&mq, p.q, kHalf, D, {p.group, p.tokens, p.kv_heads},
+                            {p.q_head, p.q_tok, p.q_head * p.group}, {p.group, tp.tok_tile, 1});
+    if (rc == RA_OK)
+        rc = make_paged_map(&mk, p.kc, kHalf, D, {p.page_size, p.kv_heads, p.num_pages}, {p.lk.st, p.lk.sh, p.lk.sp},
+                            {tp.box_rows, 1, 1});
+    if (rc == RA_OK)
+        rc = make_paged_map(&mv, p.vc, kHalf, D, {p.page_size, p.kv_heads, p.num_pages}, {p.lv.st, p.lv.sh, p.lv.sp},
+                            {tp.box_rows, 1, 1});
+    if (rc != RA_OK) return rc;
+    {
+        ra::prof::Scope ps(ra::prof::kPagedTiles, s);
+        pt::paged_tiles_kernel<D, kHalf><<<blocks, pt::kThreads, pt::Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, tp);
+        ps.done();
+    }
+    ra::prof::Scope ps(ra::prof::kPagedJoin, s);
+    ra::paged::paged_join_kernel<D, kHalf, pt::kTileRows, pt::kBM><<<dim3(blocks, pt::kTileRows / 16), 256, 0, s>>>(
+        p, tp.ws, blocks, tp.tok_tile * p.group, pt::kShift<kHalf>);
+    ps.done();
+    const cudaError_t ce = cudaGetLastError();
+    return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged_tiles_kernel launch");
+}
+
+template <int D, bool kHalf>
+int launch_attn(const ra::paged::AttnParams& p, void* workspace, int max_q, int blocks, cudaStream_t s)
+{
+    // Both kernels can serve any request, so a wrong hint costs time only.
+    if ((long long)max_q * p.group <= kFewRows || (long long)p.tokens * p.group <= kFewRows)
+        return launch_rows<D, kHalf>(p, workspace, {0, INT_MAX}, blocks, s);
+    char* tile_space = static_cast<char*>(workspace) + align256(ra::paged::workspace_bytes(ra::paged::rows::kRows, D));
+    if (p.group <= kFewRows) {
+        const int rc = launch_rows<D, kHalf>(p, workspace, {0, kFewRows}, blocks, s);
+        if (rc != RA_OK) return rc;
+    }
+    return launch_tiles<D, kHalf>(p, tile_space, {p.group <= kFewRows ? kFewRows : 0, INT_MAX}, blocks, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -70,7 +171,7 @@ int paged_kv_plan(const int* seq_lens, const int* new_lens, int n, int* block_ta
     if (rc != RA_OK) return rc;
     if (max_pages < 1 || table_stride < max_pages) return RA_ERR_INVALID_ARG;
     if (n > ra::paged::kMaxRequests || (long long)n * max_pages > (1ll << 30) || num_pages > (1 << 30) ||
-        (long long)max_pages * page_size >= (1ll << 31))
+        (long long)max_pages * page_size > (1ll << 30))
         return RA_ERR_UNSUPPORTED;
     if (n == 0 && tokens == 0) return RA_OK;
     if (!free_list || !counts || !counts_out || !cu_q || (tokens > 0 && !slots) ||
@@ -136,7 +237,9 @@ int paged_kv_append(const void* k, const long long* k_strides, const void* v, co
 size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d)
 {
     if (n <= 0 || tokens <= 0 || H <= 0 || H_kv <= 0 || H % H_kv != 0 || (d != 64 && d != 128)) return 0;
-    return (ra::paged::rows::workspace_bytes(d) + 255) / 256 * 256;
+    const size_t few = align256(ra::paged::workspace_bytes(ra::paged::rows::kRows, d));
+    if ((long long)tokens * (H / H_kv) <= kFewRows) return few;
+    return few + align256(ra::paged::workspace_bytes(ra::paged::tiles::kTileRows, d));
 }
 
 int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cache, const long long* k_cache_strides,
@@ -153,7 +256,7 @@ int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cach
     if (rc != RA_OK) return rc;
     if (H % H_kv != 0 || max_pages < 1 || table_stride < max_pages) return RA_ERR_INVALID_ARG;
     if (H / H_kv > 128 || H > (1 << 20) || (long long)H * tokens >= (1ll << 31) ||
-        (long long)max_pages * page_size >= (1ll << 31))
+        (long long)max_pages * page_size > (1ll << 30))
         return RA_ERR_UNSUPPORTED;
     long long qs[2], os[2];
     ra::paged::PoolLayout lk, lv;
@@ -201,30 +304,12 @@ int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cach
     p.scale_log2 = (float)((double)scale * 1.4426950408889634);
     p.status = st->status;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    namespace pr = ra::paged::rows;
-    const pr::Workspace ws = pr::workspace(workspace);
-    const int blocks = std::min(st->num_sms, pr::kMaxBlocks);
-    auto launch = [&](auto kernel, auto join, int smem) {
-        const int e = allow_smem(kernel, smem);
-        if (e != RA_OK) return e;
-        {
-            ra::prof::Scope ps(ra::prof::kPagedRows, s);
-            kernel<<<blocks, pr::kThreads, smem, s>>>(p, ws);
-            ps.done();
-        }
-        ra::prof::Scope ps(ra::prof::kPagedJoin, s);
-        join<<<blocks, pr::kThreads, 0, s>>>(p, ws, blocks);
-        ps.done();
-        const cudaError_t ce = cudaGetLastError();
-        return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged attention launch");
-    };
+    const int blocks = std::min(st->num_sms, ra::paged::kMaxBlocks);
     if (d == 128)
-        return dtype == RA_FP16
-                   ? launch(pr::paged_rows_kernel<128, true>, pr::paged_join_kernel<128, true>, pr::Cfg<128>::kSmemBytes)
-                   : launch(pr::paged_rows_kernel<128, false>, pr::paged_join_kernel<128, false>, pr::Cfg<128>::kSmemBytes);
-    return dtype == RA_FP16
-               ? launch(pr::paged_rows_kernel<64, true>, pr::paged_join_kernel<64, true>, pr::Cfg<64>::kSmemBytes)
-               : launch(pr::paged_rows_kernel<64, false>, pr::paged_join_kernel<64, false>, pr::Cfg<64>::kSmemBytes);
+        return dtype == RA_FP16 ? launch_attn<128, true>(p, workspace, max_q, blocks, s)
+                                : launch_attn<128, false>(p, workspace, max_q, blocks, s);
+    return dtype == RA_FP16 ? launch_attn<64, true>(p, workspace, max_q, blocks, s)
+                            : launch_attn<64, false>(p, workspace, max_q, blocks, s);
 }
 
 }  // extern "C"

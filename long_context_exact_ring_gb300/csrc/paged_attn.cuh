@@ -116,65 +116,53 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-namespace rows {
-
-constexpr int kRows = 16;        // packed rows of a tile: one m16n8k16 operand
-constexpr int kKeys = 16;        // keys of a warp's step
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = kKeys * kWarps;   // keys of a block's step, and of the smallest piece of work
+// ---------------------------------------------------------------------------
+// Parts.  A kernel cuts its list of (request, key/value head, tile of packed
+// rows, keys) into equal, contiguous shares, one for each block.  A tile's
+// keys are cut where one share ends and the next begins, so a block has at
+// most two unfinished tiles: one that it takes over from the block before
+// (part 0) and one that it leaves to the block behind (part 1).
+// ---------------------------------------------------------------------------
 constexpr int kMaxBlocks = 256;
 
-template <int D>
-struct Cfg {
-    static constexpr int kChunkBytes = kKeys * D * 2;              // a warp's K (or V) of one step
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kWarpBytes = 2 * kChunkBytes * kStages;
-    static constexpr int kSmemBytes = kWarps * kWarpBytes;
-    static_assert(kWarpBytes >= kRows * D * 4 + 2 * kRows * 4, "a warp's state fits over its stages");
-};
-
-// A tile's keys are cut where one block's share of the work ends and the
-// next one's begins, so a block has at most two unfinished tiles: one that
-// it takes over from the block before (part 0) and one that it leaves to
-// the block behind (part 1).
 struct PartInfo {
     int req;        // -1: no such part
-    int kvh, row0;
+    int kvh, row0;  // key/value head, first packed row
     int last;       // part 0 only: its tile ends in this block
 };
 
 struct Workspace {
     PartInfo* info;   // [blocks][2]
-    float* ml;        // [blocks][2][2][kRows] reference and sum of the exponentials
-    float* acc;       // [blocks][2][kRows][D] sums, not normalized
+    float* ml;        // [blocks][2][2][tile rows] reference and sum of the exponentials
+    float* acc;       // [blocks][2][tile rows][D] sums, not normalized
 };
 
-__host__ __device__ inline size_t workspace_bytes(int D)
+// Workspace of a kernel with tiles of `rows` packed rows.
+__host__ __device__ inline size_t workspace_bytes(int rows, int D)
 {
-    return (size_t)kMaxBlocks * 2 * (sizeof(PartInfo) + (2 * kRows + (size_t)kRows * D) * 4);
+    return (size_t)kMaxBlocks * 2 * (sizeof(PartInfo) + (2 * (size_t)rows + (size_t)rows * D) * 4);
 }
 
-__host__ __device__ inline Workspace workspace(void* base)
+__host__ __device__ inline Workspace workspace(void* base, int rows)
 {
     Workspace w;
     w.info = static_cast<PartInfo*>(base);
     w.ml = reinterpret_cast<float*>(w.info + 2 * kMaxBlocks);
-    w.acc = w.ml + (size_t)kMaxBlocks * 2 * 2 * kRows;
+    w.acc = w.ml + (size_t)kMaxBlocks * 2 * 2 * rows;
     return w;
 }
 
-// One warp's running state of a tile: 16 rows, of which a thread holds two.
-template <int D>
-struct State {
-    float m[2], l[2];
-    float acc[D / 8][4];
+// Which requests a kernel serves: those with more than `above` and at most
+// `upto` packed rows.
+struct RowRange {
+    int above, upto;
+    __device__ __forceinline__ bool has(int rows) const { return rows > above && rows <= upto; }
 };
 
 // Writes kPer columns of a finished row.
 template <int kPer, bool kHalf>
 __device__ __forceinline__ void store_row(const AttnParams& p, const Request& r, int kvh, int packed, int col,
-                                          const float (&out)[kPer], float m, float l)
+                                          const float (&out)[kPer], float m, float l, float shift)
 {
     using Op = Operand<kHalf>;
     // no key, or none with a weight: O = 0, LSE = -inf
@@ -188,8 +176,78 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Request& r,
     else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
     if (col == 0)
         p.lse[(long long)head * p.tokens + r.first + tok] =
-            m == -INFINITY ? -INFINITY : (m - Op::kShift + log2f(l)) * 0.69314718055994531f;
+            m == -INFINITY ? -INFINITY : (m - shift + log2f(l)) * 0.69314718055994531f;
 }
+
+// Joins the parts of a tile that several blocks had a share of: the block
+// that began it, then those behind it, in order -- the sum does not depend
+// on which finished first.  A tile's rows come in halves of kHalfRows, of
+// which the first `used` hold packed rows.  Block (b, y) joins rows 16 y ..
+// 16 y + 15 of the tile that block b began and did not finish.
+template <int D, bool kHalf, int kTileRows, int kHalfRows>
+__global__ void __launch_bounds__(256)
+paged_join_kernel(const AttnParams p, const Workspace ws, int blocks, int used, float shift)
+{
+    const int b = blockIdx.x;
+    const PartInfo info = ws.info[2 * b + 1];
+    if (info.req < 0) return;
+    constexpr int kPer = 16 * D / 256;
+    const int row = blockIdx.y * 16 + threadIdx.x / (D / kPer), col = threadIdx.x % (D / kPer) * kPer;
+    const Request r = load_request(p, info.req);
+    const int packed = info.row0 + row / kHalfRows * used + row % kHalfRows;
+    if (row % kHalfRows >= used || packed >= r.q * p.group) return;
+    float m = -INFINITY, l = 0.f, out[kPer];
+#pragma unroll
+    for (int c = 0; c < kPer; ++c) out[c] = 0.f;
+    for (int x = b; x < blocks; ++x) {
+        const int slot = x == b ? 2 * b + 1 : 2 * x;
+        bool last = false;
+        if (x != b) {
+            const PartInfo next = ws.info[slot];
+            if (next.req < 0) continue;      // a block without work
+            last = next.last;
+        }
+        const float mx = ws.ml[(size_t)slot * 2 * kTileRows + row];
+        const float lx = ws.ml[(size_t)slot * 2 * kTileRows + kTileRows + row];
+        const float* src = ws.acc + ((size_t)slot * kTileRows + row) * D + col;
+        float v[kPer];
+#pragma unroll
+        for (int c = 0; c < kPer; c += 4) *reinterpret_cast<float4*>(v + c) = *reinterpret_cast<const float4*>(src + c);
+        if (mx != -INFINITY) {
+            const float to = max_nan(m, mx), fa = ex2_approx(m - to), fb = ex2_approx(mx - to);
+            m = to;
+            l = l * fa + lx * fb;
+#pragma unroll
+            for (int c = 0; c < kPer; ++c) out[c] = out[c] * fa + v[c] * fb;
+        }
+        if (last) break;
+    }
+    store_row<kPer, kHalf>(p, r, info.kvh, packed, col, out, m, l, shift);
+}
+
+namespace rows {
+
+constexpr int kRows = 16;        // packed rows of a tile: one m16n8k16 operand
+constexpr int kKeys = 16;        // keys of a warp's step
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kUnit = kKeys * kWarps;   // keys of a block's step, and of the smallest piece of work
+
+template <int D>
+struct Cfg {
+    static constexpr int kChunkBytes = kKeys * D * 2;              // a warp's K (or V) of one step
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kWarpBytes = 2 * kChunkBytes * kStages;
+    static constexpr int kSmemBytes = kWarps * kWarpBytes;
+    static_assert(kWarpBytes >= kRows * D * 4 + 2 * kRows * 4, "a warp's state fits over its stages");
+};
+
+// One warp's running state of a tile: 16 rows, of which a thread holds two.
+template <int D>
+struct State {
+    float m[2], l[2];
+    float acc[D / 8][4];
+};
 
 // The work is the list of (request, key/value head, tile of 16 packed rows,
 // 128 keys); every block takes an equal, contiguous share of it, so a single
@@ -201,7 +259,7 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Request& r,
 //
 // Bound by HBM: K and V are read once per 16 packed rows.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParams p, const Workspace ws)
+__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParams p, const Workspace ws, const RowRange range)
 {
     using C = Cfg<D>;
     using Op = Operand<kHalf>;
@@ -219,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
     auto units_of = [&](const Request& r) { return max(1, (r.len + kUnit - 1) / kUnit); };
     auto work_of = [&](int i) {
         const Request r = load_request(p, i);
-        return (long long)tiles_of(r) * p.kv_heads * units_of(r);
+        return range.has(r.q * p.group) ? (long long)tiles_of(r) * p.kv_heads * units_of(r) : 0ll;
     };
     const int per = (p.n + kThreads - 1) / kThreads;
     const int i0 = min(p.n, tid * per), i1 = min(p.n, i0 + per);
@@ -500,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
             for (int c = 0; c < kPer; ++c) out[c] += f * part(w)[row * D + col + c];
         }
         if (u0 == 0 && u1 == units) {
-            if (row < rows) store_row<kPer, kHalf>(p, r, kvh, row0 + row, col, out, m, l);
+            if (row < rows) store_row<kPer, kHalf>(p, r, kvh, row0 + row, col, out, m, l, Op::kShift);
         } else {
             const int slot = 2 * b + (u0 == 0);
             float* dst = ws.acc + ((size_t)slot * kRows + row) * D + col;
@@ -523,46 +581,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
         }
         __syncthreads();                     // the states are read before the stages are filled again
     }
-}
-
-// Joins the parts of a tile that several blocks had a share of: the block
-// that began it, then those behind it, in order -- the sum does not depend
-// on which finished first.
-template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads) paged_join_kernel(const AttnParams p, const Workspace ws, int blocks)
-{
-    const int b = blockIdx.x;
-    const PartInfo info = ws.info[2 * b + 1];
-    if (info.req < 0) return;
-    constexpr int kPer = kRows * D / kThreads;
-    const int row = threadIdx.x / (D / kPer), col = threadIdx.x % (D / kPer) * kPer;
-    float m = -INFINITY, l = 0.f, out[kPer];
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) out[c] = 0.f;
-    for (int x = b; x < blocks; ++x) {
-        const int slot = x == b ? 2 * b + 1 : 2 * x;
-        bool last = false;
-        if (x != b) {
-            const PartInfo next = ws.info[slot];
-            if (next.req < 0) continue;      // a block without work
-            last = next.last;
-        }
-        const float mx = ws.ml[slot * 2 * kRows + row], lx = ws.ml[slot * 2 * kRows + kRows + row];
-        const float* src = ws.acc + ((size_t)slot * kRows + row) * D + col;
-        float v[kPer];
-#pragma unroll
-        for (int c = 0; c < kPer; c += 4) *reinterpret_cast<float4*>(v + c) = *reinterpret_cast<const float4*>(src + c);
-        if (mx != -INFINITY) {
-            const float to = max_nan(m, mx), fa = ex2_approx(m - to), fb = ex2_approx(mx - to);
-            m = to;
-            l = l * fa + lx * fb;
-#pragma unroll
-            for (int c = 0; c < kPer; ++c) out[c] = out[c] * fa + v[c] * fb;
-        }
-        if (last) break;
-    }
-    const Request r = load_request(p, info.req);
-    if (info.row0 + row < r.q * p.group) store_row<kPer, kHalf>(p, r, info.kvh, info.row0 + row, col, out, m, l);
 }
 
 }  // namespace rows

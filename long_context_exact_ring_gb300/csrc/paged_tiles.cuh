@@ -1,0 +1,632 @@
+// paged_tiles.cuh -- attention of many new tokens over a paged cache, on the
+// tensor cores: the form of paged_attn_fwd for prompt chunks.
+//
+// A block holds two tiles of 128 packed rows (token, head of the group) of
+// one request and key/value head; both share every tile of 128 keys.
+//   warp 0      copies Q once and K/V tiles page by page (TMA; a page's rows
+//               are boxes of a 4-D tensor map, one lane issues one box)
+//   warp 1      tensor memory and the MMAs: S = Q K^T, O += P V
+//   warps 2-5   softmax and results of tile 0
+//   warps 6-9   the same of tile 1
+// Tensor memory (512 columns): S0/P0, S1/P1 of 128 columns, then O0, O1.
+// P, rounded to the operand type (half a step of 2^-9 or 2^-12 each; the row
+// sums take it unrounded), overwrites the first 64 columns of its S.
+//
+// The work is cut into equal, contiguous shares of (request, key/value head,
+// tile, key tile), one for each SM: with as few tiles as a single chunk of a
+// few hundred tokens has, whole tiles would leave most SMs idle.  Every role
+// walks its block's share by itself, from the same start.
+//
+// Bound by the tensor cores and the exponentials, as ring_fwd_kernel; blocks
+// of one key/value head read its keys at about the same time, from L2.
+#pragma once
+
+#include "paged_attn.cuh"
+
+namespace ra {
+namespace paged {
+namespace tiles {
+
+constexpr int kBM = 128;           // packed rows of a tile
+constexpr int kBN = 128;           // keys of a key tile
+constexpr int kTiles = 2;          // row tiles of a block
+constexpr int kTileRows = kTiles * kBM;
+constexpr int kThreads = 320;
+constexpr float kRescaleThreshold = 8.0f;   // log2 units
+
+template <int D>
+struct Cfg {
+    static constexpr int kBoxes = D / 64;                       // 64-column boxes of a tile
+    static constexpr int kBoxBytes = 64 * kBN * 2;
+    static constexpr int kTileBytes = kBN * D * 2;
+    static constexpr int kStages = D == 128 ? 2 : 4;
+    static constexpr int kOffQ = 0;
+    static constexpr int kOffK = kOffQ + kTiles * kTileBytes;
+    static constexpr int kOffV = kOffK + kStages * kTileBytes;
+    static constexpr int kOffBar = kOffV + kStages * kTileBytes;
+    static constexpr int kBarBytes = 512;
+    static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;   // + alignment slack
+    static constexpr uint32_t kTmemCols = 512;
+    static constexpr uint32_t kColS = 0;          // S_u at kColS + 128 u
+    static constexpr uint32_t kColO = 256;        // O_u at kColO + D u
+};
+
+// The weights' reference (see Operand): the running maximum may lag by up to
+// 2^8, so fp16 weights stay below 2^15.
+template <bool kHalf> constexpr float kShift = kHalf ? 7.f : 0.f;
+
+struct TileParams {
+    AttnParams a;
+    Workspace ws;
+    RowRange range;
+    int tok_tile;           // tokens of a row tile: 128 / group, rounded down
+    int box_rows;           // rows of a K/V box: the largest power of two in page_size, at most 128
+    uint64_t wait_limit_ns;
+};
+
+// A block's place in its share.
+struct Walk {
+    const TileParams& p;
+    Request r;
+    TileWork w;
+    int req, kvh, t, k0;
+    long long left;
+
+    __device__ __forceinline__ Walk(const TileParams& p_, int req_, int kvh_, int t_, int k0_, long long left_)
+        : p(p_), req(req_), kvh(kvh_), t(t_), k0(k0_), left(left_)
+    {
+        load();
+    }
+    static __device__ __forceinline__ TileWork work(const TileParams& p, const Request& r)
+    {
+        return TileWork{r.q, r.len, p.a.causal, kTiles * p.tok_tile, kBN};
+    }
+    static __device__ __forceinline__ long long units(const TileParams& p, int i)
+    {
+        const Request r = load_request(p.a, i);
+        if (!p.range.has(r.q * p.a.group)) return 0;
+        const TileWork w = work(p, r);
+        return w.before(w.tiles()) * p.a.kv_heads;
+    }
+    __device__ __forceinline__ void load()
+    {
+        r = load_request(p.a, req);
+        w = work(p, r);
+    }
+    __device__ __forceinline__ int total() const { return w.units(t); }
+    __device__ __forceinline__ int end() const { return (int)min((long long)total(), k0 + left); }
+    __device__ __forceinline__ int tok0() const { return t * w.step; }
+    // row tiles that hold tokens
+    __device__ __forceinline__ int row_tiles() const { return r.q - tok0() > p.tok_tile ? 2 : 1; }
+    // To the next piece of work; false behind the last one.
+    __device__ __forceinline__ bool next()
+    {
+        left -= end() - k0;
+        if (left == 0) return false;
+        k0 = 0;
+        if (++t < w.tiles()) return true;
+        t = 0;
+        if (++kvh < p.a.kv_heads) return true;
+        kvh = 0;
+        do {
+            ++req;
+            load();
+        } while (!p.range.has(r.q * p.a.group));    // some later request has the work that is left
+        return true;
+    }
+};
+
+__device__ __forceinline__ uint32_t bits_of(uint32_t packed, int odd) { return odd ? packed >> 16 : packed & 0xffffu; }
+template <bool kHalf> __device__ __forceinline__ float widen(uint32_t bits)
+{
+    if constexpr (kHalf) return __half2float(__ushort_as_half((unsigned short)bits));
+    else return __uint_as_float(bits << 16);
+}
+
+// O += P V of one key tile for the rows of one warp, key by key and only for
+// the keys that a row sees (see the caller).  `init`: O holds nothing yet.
+template <int D, bool kHalf>
+__device__ __noinline__ void add_seen_keys(const AttnParams& a, const int* table, int kvh, int key0, int valid, int lim,
+                                           uint32_t tS, uint32_t tO, bool init)
+{
+    for (int half = 0; half < 2; ++half) {
+        uint32_t pk[32];
+        tmem_ld32(tS + 32u * half, pk);
+        tmem_ld_wait(pk);
+        uint32_t weight[32];     // indexed at run time: lives in local memory
+        for (int c = 0; c < 32; ++c) weight[c] = pk[c];
+        for (int c4 = 0; c4 < D / 32; ++c4) {
+            uint32_t o[32];
+            if (!(init && half == 0)) {
+                tmem_ld32(tO + 32u * c4, o);
+                tmem_ld_wait(o);
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) o[c] = 0u;
+            }
+            for (int k = 0; k < 64 && 64 * half + k < valid; ++k) {
+                const int key = key0 + 64 * half + k;
+                const int pi = page_index(key, a.page_size, a.page_shift), page = table[pi];
+                if (!page_ok(page, a.num_pages)) continue;
+                const uint4* row = reinterpret_cast<const uint4*>(
+                    a.vc + row_offset(a.lv, page, key - pi * a.page_size, kvh) + 32 * c4);
+                if (key > lim) continue;
+                const float wgt = widen<kHalf>(bits_of(weight[k >> 1], k & 1));
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const uint4 x = row[v];
+                    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int z = 0; z < 8; ++z)
+                        o[8 * v + z] = __float_as_uint(fmaf(wgt, widen<kHalf>(bits_of(y[z >> 1], z & 1)),
+                                                            __uint_as_float(o[8 * v + z])));
+                }
+            }
+            __syncwarp();
+            tmem_st32(tO + 32u * c4, o);
+            tmem_st_wait();
+        }
+    }
+}
+
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                   const __grid_constant__ CUtensorMap map_v, const __grid_constant__ TileParams p)
+{
+    using CF = Cfg<D>;
+    using Op = Operand<kHalf>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ long long s_scratch[kThreads / 32 + 1];
+    __shared__ int s_start[4];             // request, key/value head, tile, key tile
+    __shared__ int s_seen[2];              // piece whose O tile u holds sums before its first MMA
+    __shared__ int s_odd[2][2];            // check whose V tile holds an infinity or a NaN
+    const uint32_t raw_base = smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw_base);
+    const uint32_t sQ = base + CF::kOffQ, sK = base + CF::kOffK, sV = base + CF::kOffV;
+    const uint32_t bar0 = base + CF::kOffBar;
+    const uint32_t bar_q_full = bar0, bar_q_empty = bar0 + 8u;
+    auto bar_k_full = [&](int s) { return bar0 + 8u * (2 + s); };
+    auto bar_k_empty = [&](int s) { return bar0 + 8u * (2 + CF::kStages + s); };
+    auto bar_v_full = [&](int s) { return bar0 + 8u * (2 + 2 * CF::kStages + s); };
+    auto bar_v_empty = [&](int s) { return bar0 + 8u * (2 + 3 * CF::kStages + s); };
+    const uint32_t bar_misc = bar0 + 8u * (2 + 4 * CF::kStages);
+    auto bar_s_full = [&](int u) { return bar_misc + 8u * u; };          // MMA -> softmax
+    auto bar_p_full = [&](int u) { return bar_misc + 8u * (2 + u); };    // softmax -> MMA
+    const uint32_t bar_o_final = bar_misc + 8u * 4;                      // last P V of a piece done
+    const uint32_t bar_drain = bar_misc + 8u * 5;
+    auto bar_check = [&](int two) { return bar_misc + 8u * (6 + two); }; // V checked by one or both groups
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + CF::kOffBar + 448);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + CF::kOffBar + 456);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const AttnParams& a = p.a;
+
+    // ---- this block's share of the work
+    const int G = gridDim.x, b = blockIdx.x;
+    const int per = (a.n + kThreads - 1) / kThreads;
+    const int i0 = min(a.n, tid * per), i1 = min(a.n, i0 + per);
+    long long mine = 0, total;
+    for (int i = i0; i < i1; ++i) mine += Walk::units(p, i);
+    const long long before = block_exclusive_sum(mine, s_scratch, &total);
+    const long long share = total / G + (b < total % G);
+    const long long start = total / G * b + min((long long)b, total % G);
+    if (tid < 2) p.ws.info[2 * b + tid].req = -1;
+    if (share == 0) return;
+    if (before <= start && start < before + mine) {
+        long long x = start - before;
+        int i = i0;
+        for (long long c; x >= (c = Walk::units(p, i)); ++i) x -= c;
+        const TileWork w = Walk::work(p, load_request(a, i));
+        const long long head = w.before(w.tiles());
+        s_start[0] = i;
+        s_start[1] = (int)(x / head);
+        x %= head;
+        s_start[2] = w.tile_of(x);
+        s_start[3] = (int)(x - w.before(s_start[2]));
+    }
+
+    WaitCtl wc{abort_flag, a.status, p.wait_limit_ns};
+    if (tid == 0) {
+        *abort_flag = 0;
+        mbar_init(bar_q_full, 1);
+        mbar_init(bar_q_empty, 1);
+        for (int s = 0; s < CF::kStages; ++s) {
+            mbar_init(bar_k_full(s), 1);
+            mbar_init(bar_k_empty(s), 1);
+            mbar_init(bar_v_full(s), 1);
+            mbar_init(bar_v_empty(s), 1);
+        }
+        for (int u = 0; u < kTiles; ++u) {
+            mbar_init(bar_s_full(u), 1);
+            mbar_init(bar_p_full(u), kBM);
+            mbar_init(bar_check(u), kBM * (1 + u));
+            s_seen[u] = 0;
+            s_odd[u][0] = s_odd[u][1] = 0;
+        }
+        mbar_init(bar_o_final, 1);
+        mbar_init(bar_drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), CF::kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    Walk walk(p, s_start[0], s_start[1], s_start[2], s_start[3], share);
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        const int boxes = kBN / p.box_rows * CF::kBoxes;     // at most 32: one for each lane
+        const int box = lane / CF::kBoxes, half = lane % CF::kBoxes;
+        const uint32_t box_dst = (uint32_t)(half * CF::kBoxBytes + box * p.box_rows * 128);
+        const uint32_t q_bytes = (uint32_t)(p.tok_tile * a.group * 128 * CF::kBoxes);
+        if (lane == 0) {
+            tma_prefetch_desc(&map_q);
+            tma_prefetch_desc(&map_k);
+            tma_prefetch_desc(&map_v);
+        }
+        int last_k[CF::kStages], last_v[CF::kStages], last_q = -1;   // parity of the last copy issued
+        for (int s = 0; s < CF::kStages; ++s) last_k[s] = last_v[s] = -1;
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+        };
+        bool ok = true;
+        uint32_t n = 0, piece = 0;
+        do {
+            const int* table = a.table + (long long)walk.req * a.table_stride;
+            const int keys = walk.w.keys(walk.t), k1 = walk.end(), nu = walk.row_tiles();
+            auto page_at = [&](int kt) {
+                const int key = kt * kBN + box * p.box_rows;
+                return lane < boxes && kt < k1 && key < keys
+                           ? table[page_index(key, a.page_size, a.page_shift)] : 0;
+            };
+            int page = page_at(walk.k0);
+            if (!(ok = wait_all(bar_q_empty, (piece & 1u) ^ 1u))) break;
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar_q_full, q_bytes * nu);
+                for (int u = 0; u < nu; ++u)
+                    for (int x = 0; x < CF::kBoxes; ++x)
+                        tma_load_4d(sQ + u * CF::kTileBytes + x * CF::kBoxBytes, &map_q, bar_q_full, 64 * x, 0,
+                                    walk.r.first + walk.tok0() + u * p.tok_tile, walk.kvh);
+            }
+            last_q = (int)(piece & 1u);
+            for (int kt = walk.k0; kt < k1; ++kt, ++n) {
+                const int s = n % CF::kStages;
+                const uint32_t ph = (n / CF::kStages) & 1u;
+                const int key = kt * kBN + box * p.box_rows;
+                const bool load = lane < boxes && key < keys;
+                // a page outside the pool: a coordinate outside the map, which reads as zeros
+                int coord = page;
+                if (load && !page_ok(page, a.num_pages)) {
+                    coord = a.num_pages;
+                    atomicOr(a.status, kStatusBadPage);
+                }
+                const int off = key - page_index(key, a.page_size, a.page_shift) * a.page_size;
+                page = page_at(kt + 1);
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * p.box_rows * 128u;
+                if (!(ok = wait_all(bar_k_empty(s), ph ^ 1u))) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar_k_full(s), bytes);
+                __syncwarp();
+                if (load)
+                    tma_load_4d(sK + s * CF::kTileBytes + box_dst, &map_k, bar_k_full(s), 64 * half, off, walk.kvh, coord);
+                last_k[s] = (int)ph;
+                if (!(ok = wait_all(bar_v_empty(s), ph ^ 1u))) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar_v_full(s), bytes);
+                __syncwarp();
+                if (load)
+                    tma_load_4d(sV + s * CF::kTileBytes + box_dst, &map_v, bar_v_full(s), 64 * half, off, walk.kvh, coord);
+                last_v[s] = (int)ph;
+            }
+            ++piece;
+        } while (ok && walk.next());
+        if (!ok) {
+            // Let every copy still in flight land before the block exits.
+            volatile int dummy = 0;
+            WaitCtl drain{&dummy, a.status, 200000000ull};
+            if (last_q >= 0) mbar_wait(bar_q_full, (uint32_t)last_q, drain);
+            for (int s = 0; s < CF::kStages; ++s) {
+                if (last_k[s] >= 0) mbar_wait(bar_k_full(s), (uint32_t)last_k[s], drain);
+                if (last_v[s] >= 0) mbar_wait(bar_v_full(s), (uint32_t)last_v[s], drain);
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------------------------------------- MMA
+        // The whole warp runs converged; one elected lane issues the MMAs and
+        // commits.  MMAs run in the order of issue, so the next S = Q K^T,
+        // issued after P V, does not overwrite P early.
+        constexpr uint32_t kType = kHalf ? 0u : (1u << 7) | (1u << 10);
+        constexpr uint32_t kTypeMask = ~((1u << 7) | (1u << 10));
+        constexpr uint32_t idesc_qk = (idesc_bf16_f32(kBM, kBN, false, false) & kTypeMask) | kType;
+        constexpr uint32_t idesc_pv = (idesc_bf16_f32(kBM, D, false, true) & kTypeMask) | kType;
+        const uint64_t dq0 = sdesc_sw128(sQ, 16, 1024);
+        const uint64_t dk0 = sdesc_sw128(sK, 16, 1024);
+        const uint64_t dv0 = sdesc_sw128(sV, CF::kBoxBytes, 1024);
+        constexpr uint32_t kTile16 = CF::kTileBytes >> 4, kBox16 = CF::kBoxBytes >> 4;
+        auto issue_s = [&](int u, int s) {
+            const uint64_t dq = dq0 + (uint32_t)u * kTile16, dk = dk0 + (uint32_t)s * kTile16;
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off16 = (kk >> 2) * kBox16 + (kk & 3) * 2;
+                    mma_bf16_ss(tmem + CF::kColS + 128u * u, dq + off16, dk + off16, idesc_qk, kk > 0 ? 1u : 0u);
+                }
+            }
+            __syncwarp();
+        };
+        auto issue_pv = [&](int u, int s, bool first) {
+            const uint64_t dv = dv0 + (uint32_t)s * kTile16;
+            if (elect_one()) {
+#pragma unroll
+                for (int kk = 0; kk < kBN / 16; ++kk)
+                    mma_bf16_ts(tmem + CF::kColO + (uint32_t)D * u, tmem + CF::kColS + 128u * u + 8u * kk,
+                                dv + (uint32_t)kk * (2048 >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
+            }
+            __syncwarp();
+        };
+        auto commit = [&](uint32_t bar) {
+            if (elect_one()) mma_commit(bar);
+            __syncwarp();
+        };
+        auto wait_all = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+        };
+        bool ok = true;
+        uint32_t n = 0, piece = 0, done[2] = {0, 0};      // key tiles; pieces; weights of tile u taken
+        do {
+            const int count = walk.end() - walk.k0, nu = walk.row_tiles();
+            const int s0 = n % CF::kStages;
+            if (!(ok = wait_all(bar_q_full, piece & 1u) && wait_all(bar_k_full(s0), (n / CF::kStages) & 1u))) break;
+            tc_fence_after();
+            for (int u = 0; u < nu; ++u) {
+                issue_s(u, s0);
+                commit(bar_s_full(u));
+            }
+            commit(bar_k_empty(s0));
+            if (count == 1) commit(bar_q_empty);
+            for (int j = 0; j < count && ok; ++j, ++n) {
+                const int s = n % CF::kStages, s1 = (n + 1) % CF::kStages;
+                const bool more = j + 1 < count;
+                if (!(ok = wait_all(bar_v_full(s), (n / CF::kStages) & 1u))) break;
+                for (int u = 0; u < nu; ++u) {
+                    if (!(ok = wait_all(bar_p_full(u), done[u] & 1u))) break;
+                    ++done[u];
+                    tc_fence_after();
+                    const bool first = j == 0 && *(volatile int*)&s_seen[u] != (int)(piece + 1);
+                    issue_pv(u, s, first);
+                    if (u == nu - 1) commit(bar_v_empty(s));
+                    if (more) {
+                        if (u == 0) {
+                            if (!(ok = wait_all(bar_k_full(s1), ((n + 1) / CF::kStages) & 1u))) break;
+                            tc_fence_after();
+                        }
+                        issue_s(u, s1);
+                        commit(bar_s_full(u));
+                        if (u == nu - 1) {
+                            commit(bar_k_empty(s1));
+                            if (j + 2 == count) commit(bar_q_empty);
+                        }
+                    }
+                }
+            }
+            if (ok) commit(bar_o_final);
+            ++piece;
+        } while (ok && walk.next());
+        // Every MMA issued so far must finish before tensor memory is released.
+        commit(bar_drain);
+        volatile int dummy = 0;
+        WaitCtl drain{&dummy, a.status, 200000000ull};
+        __all_sync(0xffffffffu, mbar_wait(bar_drain, 0, drain));
+    } else {
+        // ------------------------------------------------- softmax + results
+        const int u = (warp - 2) >> 2;                 // row tile
+        const uint32_t quarter = (uint32_t)(warp & 3); // tensor memory lane quarter
+        const int row = (int)quarter * 32 + lane;
+        const uint32_t tS = tmem_addr(tmem, quarter * 32, CF::kColS + 128u * u);
+        const uint32_t tO = tmem_addr(tmem, quarter * 32, CF::kColO + (uint32_t)D * u);
+        const float sl2 = a.scale_log2;
+        const int used = p.tok_tile * a.group;
+        bool ok = true;
+        uint32_t n = 0, piece = 0, seen = 0, checks[2] = {0, 0};
+        do {
+            const int k1 = walk.end(), nu = walk.row_tiles(), keys = walk.w.keys(walk.t);
+            const int packed = walk.tok0() * a.group + u * used + row;
+            const int tok = packed / a.group;
+            const bool store = row < used && tok < walk.r.q;
+            // last key that the row, the block's first row and the tile's first row see
+            const int past = walk.r.len - walk.r.q;
+            const int lim = a.causal ? past + min(tok, walk.r.q - 1) : walk.r.len - 1;
+            const int lim_block = a.causal ? past + walk.tok0() : walk.r.len - 1;
+            const int lim_tile = a.causal ? past + walk.tok0() + u * p.tok_tile : walk.r.len - 1;
+            float m_used = -INFINITY;   // reference of the exponentials (log2), without the shift
+            float l = 0.f;
+            if (u < nu) {
+                for (int kt = walk.k0; kt < k1; ++kt, ++n, ++seen) {
+                    // all lanes leave together: the tcgen05 loads below are warp-wide
+                    ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(u), seen & 1u, wc));
+                    if (!ok) break;
+                    tc_fence_after();
+                    uint32_t s[128];
+#pragma unroll
+                    for (int c4 = 0; c4 < 4; ++c4)
+                        tmem_ld32(tS + 32u * c4, *reinterpret_cast<uint32_t(*)[32]>(&s[32 * c4]));
+                    tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[0]));
+                    tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[32]));
+                    tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[64]));
+                    tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                    const int key0 = kt * kBN;
+                    if (key0 + kBN - 1 > lim_tile) {
+                        const int last = lim - key0;
+#pragma unroll
+                        for (int c = 0; c < 128; ++c)
+                            if (c > last) s[c] = __float_as_uint(-INFINITY);
+                    }
+                    // Row maximum: four independent chains of 3-input maxima.
+                    float mq[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) mq[x] = __uint_as_float(s[x]);
+#pragma unroll
+                    for (int c = 4; c < 124; c += 8) {
+#pragma unroll
+                        for (int x = 0; x < 4; ++x)
+                            mq[x] = max3f(mq[x], __uint_as_float(s[c + 2 * x]), __uint_as_float(s[c + 2 * x + 1]));
+                    }
+                    mq[0] = max3f(mq[0], __uint_as_float(s[124]), __uint_as_float(s[125]));
+                    mq[1] = max3f(mq[1], __uint_as_float(s[126]), __uint_as_float(s[127]));
+                    const float m_new = max3f(mq[0], mq[1], fmaxf(mq[2], mq[3])) * sl2;
+                    // The reference is raised only when the maximum is above
+                    // it by more than 2^8; O and l share it, so results are exact.
+                    const bool raise = m_new > m_used + kRescaleThreshold;
+                    float alpha = 1.f;
+                    if (raise) {
+                        alpha = ex2_approx(m_used - m_new);   // 0 when m_used = -inf
+                        m_used = m_new;
+                    }
+                    const float mb = m_used == -INFINITY ? 0.f : m_used - kShift<kHalf>;
+                    float sp[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c = 0; c < 128; c += 2) {
+                        const float p0 = ex2_approx(fmaf(__uint_as_float(s[c]), sl2, -mb));
+                        const float p1 = ex2_approx(fmaf(__uint_as_float(s[c + 1]), sl2, -mb));
+                        const int x = (c >> 1) & 1;
+                        sp[2 * x] += p0;
+                        sp[2 * x + 1] += p1;
+                        s[c >> 1] = Op::pack(p0, p1);
+                    }
+                    tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(&s[0]));
+                    tmem_st32(tS + 32u, *reinterpret_cast<const uint32_t(*)[32]>(&s[32]));
+                    l = l * alpha + ((sp[0] + sp[1]) + (sp[2] + sp[3]));
+                    if (kt > walk.k0 && __any_sync(0xffffffffu, raise)) {
+                        // O_u is idle: the S_u just read was issued after the last
+                        // P_u V, and its completion covers every earlier MMA.
+#pragma unroll
+                        for (int c4 = 0; c4 < D / 32; ++c4) {
+                            uint32_t o[32];
+                            tmem_ld32(tO + 32u * c4, o);
+                            tmem_ld_wait(o);
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                            tmem_st32(tO + 32u * c4, o);
+                        }
+                    }
+                    tmem_st_wait();
+                    if (key0 + kBN - 1 > lim_block) {
+                        // Some row does not see some key of this tile, and a
+                        // weight of 0 does not hide an infinity or a NaN in
+                        // V.  Rows of V behind the last key in use, which may
+                        // never have been written, are cleared; and if a row
+                        // in use holds one, all of V is cleared and the keys
+                        // are added one by one to the rows that see them.
+                        const int two = nu - 1, group_threads = kBM * nu, me = tid - 64;
+                        const int vs = n % CF::kStages, valid = min(kBN, keys - key0);
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(vs), (n / CF::kStages) & 1u, wc));
+                        if (!ok) break;
+                        const uint32_t v = sV + vs * CF::kTileBytes;
+                        volatile int* odd_slot = &s_odd[two][checks[two] & 1u];
+                        const int check = (int)checks[two] + 1;
+                        bool odd = false;
+                        for (int x = me; x < kBN * D / 8; x += group_threads) {
+                            uint4* at = reinterpret_cast<uint4*>(gbase + (v - base) + x * 16);
+                            if (((x >> 3) & (kBN - 1)) >= valid) {
+                                *at = make_uint4(0u, 0u, 0u, 0u);
+                            } else {
+                                const uint4 y = *at;
+                                odd |= Op::nonfinite(y.x) || Op::nonfinite(y.y) || Op::nonfinite(y.z) || Op::nonfinite(y.w);
+                            }
+                        }
+                        if (odd) *odd_slot = check;
+                        fence_proxy_async_smem();
+                        mbar_arrive(bar_check(two));
+                        ok = __all_sync(0xffffffffu, mbar_wait(bar_check(two), checks[two] & 1u, wc));
+                        ++checks[two];
+                        if (!ok) break;
+                        if (*odd_slot == check) {
+                            for (int x = me; x < kBN * D / 8; x += group_threads)
+                                *reinterpret_cast<uint4*>(gbase + (v - base) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                            mbar_arrive(bar_check(two));
+                            ok = __all_sync(0xffffffffu, mbar_wait(bar_check(two), checks[two] & 1u, wc));
+                            ++checks[two];
+                            if (!ok) break;
+                            add_seen_keys<D, kHalf>(a, a.table + (long long)walk.req * a.table_stride, walk.kvh, key0,
+                                                    valid, lim, tS, tO, kt == walk.k0);
+                            if (kt == walk.k0) *(volatile int*)&s_seen[u] = (int)(piece + 1);
+                        }
+                    }
+                    tc_fence_before();
+                    mbar_arrive(bar_p_full(u));
+                }
+            } else {
+                n += (uint32_t)(k1 - walk.k0);
+            }
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_o_final, piece & 1u, wc));
+            if (ok && u < nu) {
+                tc_fence_after();
+                const bool whole = walk.k0 == 0 && k1 == walk.total();
+                if (whole) {
+                    const bool none = m_used == -INFINITY && l == 0.f;    // no key with a weight
+                    const float inv = none ? 0.f : 1.f / l;
+                    const int head = walk.kvh * a.group + (packed - tok * a.group);
+                    uint16_t* dst = a.o + (long long)(walk.r.first + tok) * a.o_tok + (long long)head * a.o_head;
+#pragma unroll
+                    for (int c4 = 0; c4 < D / 32; ++c4) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32u * c4, o);
+                        tmem_ld_wait(o);
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            pk[c] = Op::pack(__uint_as_float(o[2 * c]) * inv, __uint_as_float(o[2 * c + 1]) * inv);
+                        if (store) {
+                            uint4* d4 = reinterpret_cast<uint4*>(dst + 32 * c4);
+#pragma unroll
+                            for (int x = 0; x < 4; ++x)
+                                d4[x] = make_uint4(pk[4 * x], pk[4 * x + 1], pk[4 * x + 2], pk[4 * x + 3]);
+                        }
+                    }
+                    if (store)
+                        a.lse[(long long)head * a.tokens + walk.r.first + tok] =
+                            none ? -INFINITY : (m_used - kShift<kHalf> + log2f(l)) * 0.69314718055994531f;
+                } else {
+                    const int slot = 2 * b + (walk.k0 == 0);
+                    const size_t prow = (size_t)slot * kTileRows + u * kBM + row;
+#pragma unroll
+                    for (int c4 = 0; c4 < D / 32; ++c4) {
+                        uint32_t o[32];
+                        tmem_ld32(tO + 32u * c4, o);
+                        tmem_ld_wait(o);
+                        float4* d4 = reinterpret_cast<float4*>(p.ws.acc + prow * D + 32 * c4);
+#pragma unroll
+                        for (int x = 0; x < 8; ++x)
+                            d4[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+                    }
+                    // a NaN sum without a maximum (every score NaN) must not read as "no key"
+                    float* ml = p.ws.ml + (size_t)slot * 2 * kTileRows + u * kBM + row;
+                    ml[0] = l == l ? m_used : l;
+                    ml[kTileRows] = l;
+                    if (row == 0 && u == 0)
+                        p.ws.info[slot] = PartInfo{walk.req, walk.kvh, walk.tok0() * a.group, k1 == walk.total()};
+                }
+            }
+            ++piece;
+        } while (ok && walk.next());
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, CF::kTmemCols);
+    }
+}
+
+}  // namespace tiles
+}  // namespace paged
+}  // namespace ra

@@ -18,14 +18,15 @@ namespace ra {
 namespace prof {
 
 enum Kind : int { kFwd = 0, kBwdMain, kBwdPrep, kDqConvert, kMerge, kInConvert, kPagedPlan,
-                  kPagedAppend, kPagedRows, kPagedJoin, kKinds };
+                  kPagedAppend, kPagedRows, kPagedJoin, kPagedTiles, kKinds };
 
 inline const char* kind_name(int k)
 {
     static const char* names[kKinds] = {"ring_fwd_kernel", "ring_bwd_kernel", "bwd_prep_kernel",
                                         "dq_convert_kernel", "merge_partials_kernel",
                                         "f32_to_bf16_kernel", "paged_plan_kernel",
-                                        "paged_append_kernel", "paged_rows_kernel", "paged_join_kernel"};
+                                        "paged_append_kernel", "paged_rows_kernel", "paged_join_kernel",
+                                        "paged_tiles_kernel"};
     return (k >= 0 && k < kKinds) ? names[k] : "";
 }
 

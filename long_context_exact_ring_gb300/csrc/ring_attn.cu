@@ -18,6 +18,7 @@
 #include "bwd_kernel.cuh"
 #include "small_kernels.cuh"
 #include "paged_attn.cuh"
+#include "paged_tiles.cuh"
 
 namespace {
 

@@ -76,7 +76,7 @@ def _attn(ra, q=FAKE, qs=None, kc=FAKE, cs=None, table=FAKE, stride=8, o=FAKE, l
 @pytest.mark.parametrize("change,code", [
     (dict(n=-1), -1), (dict(tokens=-1), -1), (dict(H=0), -1), (dict(H=9), -1), (dict(Hkv=0), -1), (dict(d=96), -2),
     (dict(d=256), -2), (dict(ps=17), -2), (dict(pages=0), -1), (dict(max_pages=0), -1), (dict(stride=7), -1),
-    (dict(max_q=-1), -1), (dict(causal=2), -1), (dict(scale=0.0), -1), (dict(scale=-1.0), -1),
+    (dict(max_pages=1 << 27, stride=1 << 27), -2), (dict(max_q=-1), -1), (dict(causal=2), -1), (dict(scale=0.0), -1), (dict(scale=-1.0), -1),
     (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(dtype=2), -1),
     (dict(H=258, Hkv=2), -2), (dict(tokens=1 << 30), -2), (dict(pages=1 << 27), -2), (dict(q=0), -1),
     (dict(q=FAKE + 8), -1), (dict(kc=FAKE + 4), -1), (dict(o=0), -1), (dict(lse=FAKE + 2), -1), (dict(table=0), -1),
@@ -141,6 +141,27 @@ int main()
             if (page_index(key, 1 << s, s) != page_index(key, 1 << s, -1)) return 5;
     for (int page : odd)
         if (page_ok(page, 41) != (page >= 0 && page < 41)) return 6;
+    // shares of the work: sums of a request's tiles against the tiles one by one
+    for (int q : {1, 31, 32, 33, 64, 100, 509, 1500})
+        for (int len : {0, 1, 5, 63, 64, 65, 128, 500, 509, 512, 4096, 131072})
+            for (int causal : {0, 1}) for (int step : {1, 2, 36, 64, 256}) for (int unit : {16, 128}) {
+                const TileWork w{q, len, causal, step, unit};
+                long long sum = 0;
+                for (int t = 0; t < w.tiles(); ++t) {
+                    if (w.before(t) != sum) { std::printf("sum %d %d %d %d\n", q, len, step, t); return 8; }
+                    if (w.tile_of(sum) != t || w.tile_of(sum + w.units(t) - 1) != t) return 9;
+                    int seen = causal ? len - q + ((t + 1) * step < q ? (t + 1) * step : q) : len;
+                    if (seen < 0) seen = 0;
+                    if (w.units(t) < 1 || w.units(t) * unit < seen || (w.units(t) > 1 && (w.units(t) - 1) * unit >= seen))
+                        return 10;
+                    sum += w.units(t);
+                }
+                if (w.before(w.tiles()) != sum) return 11;
+            }
+    {   // the largest that the calls accept
+        const TileWork w{1 << 30, 1 << 30, 1, 1, 16};
+        if (w.before(w.tiles()) <= 0 || w.tile_of(w.before(w.tiles()) - 1) != w.tiles() - 1) return 12;
+    }
     // rows past 2^32 elements, and a row behind the last page never named
     const PoolLayout l{8ll * 16 * 128, 128, 16 * 128};
     if (row_offset(l, 1 << 20, 15, 7) != (1ll << 20) * l.sp + 15 * 128 + 7ll * 16 * 128) return 7;
