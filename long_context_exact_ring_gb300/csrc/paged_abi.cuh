@@ -46,6 +46,14 @@ int check_pool(int num_pages, int page_size, int H_kv, int d)
     return RA_OK;
 }
 
+// log2 of a power of two, else -1
+int page_shift(int page_size)
+{
+    for (int x = 0; x < 31; ++x)
+        if (page_size == (1 << x)) return x;
+    return -1;
+}
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Once per device, before the first launch of a kernel with this much
@@ -185,17 +193,32 @@ int paged_kv_plan(const int* seq_lens, const int* new_lens, int n, int* block_ta
     if (e != RA_OK) return e;
     ra::paged::PlanParams p{seq_lens,     new_lens, block_table, table_stride, free_list, counts, seq_lens_out,
                             cu_q,         slots,    counts_out,  n,            max_pages, num_pages, page_size,
-                            tokens};
+                            page_shift(page_size), tokens};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t smem = ra::paged::plan_smem(n);
     if (smem > 48 * 1024) {
         e = allow_smem(ra::paged::paged_plan_kernel, (int)ra::paged::plan_smem(ra::paged::kMaxRequests));
         if (e != RA_OK) return e;
     }
-    ra::prof::Scope ps(ra::prof::kPagedPlan, s);
-    ra::paged::paged_plan_kernel<<<1, ra::paged::kPlanThreads, smem, s>>>(p);
-    ps.done();
-    const cudaError_t ce = cudaGetLastError();
+    const unsigned blocks = ra::paged::kPlanCluster;
+    cudaError_t ce = cudaFuncSetAttribute(ra::paged::paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (ce == cudaSuccess) {
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = blocks;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(blocks);
+        cfg.blockDim = dim3(ra::paged::kPlanThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        ra::prof::Scope ps(ra::prof::kPagedPlan, s);
+        ce = cudaLaunchKernelEx(&cfg, ra::paged::paged_plan_kernel, p);
+        ps.done();
+    }
+    if (ce != cudaSuccess) cudaGetLastError();    // reported here, not by a later call
     return ce == cudaSuccess ? RA_OK : fail_cuda(ce, "paged_plan_kernel launch");
 }
 
@@ -295,9 +318,7 @@ int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cach
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.page_size = page_size;
-    p.page_shift = -1;
-    for (int x = 0; x < 31; ++x)
-        if (page_size == (1 << x)) p.page_shift = x;
+    p.page_shift = page_shift(page_size);
     p.kv_heads = H_kv;
     p.group = H / H_kv;
     p.causal = causal;

@@ -285,8 +285,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
     for (int i = i0; i < i1; ++i) mine += work_of(i);
     const long long before = block_exclusive_sum(mine, s_scratch, &total);
     const int G = gridDim.x, b = blockIdx.x;
-    long long left = total / G + (b < total % G);                    // units of this block
-    const long long start = total / G * b + min((long long)b, total % G);
+    const Share share = share_of(total, G, b);
+    const long long start = share.start;
+    long long left = share.count;
     if (tid < 2) ws.info[2 * b + tid].req = -1;
     if (left == 0) return;
     if (before <= start && start < before + mine) {

@@ -53,19 +53,56 @@ RA_HD long long row_offset(const PoolLayout& l, int page, int offset, int head)
     return page * l.sp + offset * l.st + head * l.sh;
 }
 
+// Block b's share of `total` units over `blocks` (at most 2^16) equal blocks:
+// units [start, start + count).  Divides 16 bits at a time: a 64-bit division
+// is a function call on the GPU.
+struct Share {
+    long long start, count;
+};
+
+RA_HD Share share_of(long long total, int blocks, int b)
+{
+    unsigned long long quotient = 0;
+    unsigned rest = 0;
+    for (int x = 48; x >= 0; x -= 16) {
+        const unsigned part = rest << 16 | (unsigned)((unsigned long long)total >> x & 0xffffu);
+        quotient = quotient << 16 | part / (unsigned)blocks;
+        rest = part % (unsigned)blocks;
+    }
+    const long long each = (long long)quotient, over = (long long)rest;
+    Share s;
+    s.start = each * b + (b < over ? b : over);
+    s.count = each + (b < over ? 1 : 0);
+    return s;
+}
+
+// x / size of a quotient below `count`, by bisection.
+RA_HD int quotient_below(long long x, long long size, int count)
+{
+    int lo = 0, hi = count;
+    while (hi - lo > 1) {
+        const int mid = lo + (hi - lo) / 2;
+        if (mid * size <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
 // sum over i in [0, n) of floor((a i + b) / m), by Euclid's steps on (a, m).
-RA_HD long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a, unsigned long long b)
+// a n + b and the quotients' top values stay below 2^32.
+RA_HD long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b)
 {
     unsigned long long sum = 0;
     while (true) {
-        sum += n * (n - 1) / 2 * (a / m) + n * (b / m);
-        a %= m;
-        b %= m;
-        const unsigned long long top = a * n + b;
+        const unsigned qa = a / m, qb = b / m;
+        sum += (unsigned long long)n * (n - 1) / 2 * qa + (unsigned long long)n * qb;
+        a -= qa * m;
+        b -= qb * m;
+        const unsigned top = a * n + b;
         if (top < m) return (long long)sum;
         n = top / m;
-        b = top % m;
-        const unsigned long long x = a;
+        b = top - n * m;
+        const unsigned x = a;
         a = m;
         m = x;
     }
@@ -95,19 +132,18 @@ struct TileWork {
     {
         if (t <= 0) return 0;
         if (!causal) return (long long)t * units(0);
-        if (t == tiles()) return before(t - 1) + units(t - 1);
+        // the last tile may be short: it comes on top
+        const int last = t == tiles() ? units(--t) : 0;
         // tiles 0 .. t-1 end at token (i + 1) step: units 1 + (first + i step) / unit
         // from the first tile on that sees a key
-        const long long first = (long long)len - q + step - 1;
-        const long long blind = first < 0 ? (-first + step - 1) / step : 0;
-        if (t <= blind) return t;
-        return t + floor_sum((unsigned long long)(t - blind), (unsigned long long)unit, (unsigned long long)step,
-                             (unsigned long long)(first + blind * step));
+        const int first = len - q + step - 1;
+        const int blind = first < 0 ? (-first + step - 1) / step : 0;
+        if (t <= blind) return t + last;
+        return t + last + floor_sum((unsigned)(t - blind), (unsigned)unit, (unsigned)step, (unsigned)(first + blind * step));
     }
-    // the tile that unit x of the request's tiles lies in, 0 <= x < before(tiles())
-    RA_HD int tile_of(long long x) const
+    // the tile that unit x lies in, out of tiles [lo, hi), before(lo) <= x < before(hi)
+    RA_HD int tile_of(long long x, int lo, int hi) const
     {
-        int lo = 0, hi = tiles();
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (before(mid) <= x) lo = mid;

@@ -6,8 +6,10 @@
 //   warp 0      copies Q once and K/V tiles page by page (TMA; a page's rows
 //               are boxes of a 4-D tensor map, one lane issues one box)
 //   warp 1      tensor memory and the MMAs: S = Q K^T, O += P V
-//   warps 2-5   softmax and results of tile 0
-//   warps 6-9   the same of tile 1
+//   warps 2-3   nothing: they lend their registers to the warps below, whose
+//               128 scores each would not fit in an even share
+//   warps 4-7   softmax and results of tile 0
+//   warps 8-11  the same of tile 1
 // Tensor memory (512 columns): S0/P0, S1/P1 of 128 columns, then O0, O1.
 // P, rounded to the operand type (half a step of 2^-9 or 2^-12 each; the row
 // sums take it unrounded), overwrites the first 64 columns of its S.
@@ -31,7 +33,10 @@ constexpr int kBM = 128;           // packed rows of a tile
 constexpr int kBN = 128;           // keys of a key tile
 constexpr int kTiles = 2;          // row tiles of a block
 constexpr int kTileRows = kTiles * kBM;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// Registers of warps 0-3 and of warps 4-11: 128 * 56 + 256 * 224 are the 384 *
+// 168 that the block starts with.
+constexpr int kFewRegs = 88, kManyRegs = 208;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
 template <int D>
@@ -126,15 +131,17 @@ template <bool kHalf> __device__ __forceinline__ float widen(uint32_t bits)
 // O += P V of one key tile for the rows of one warp, key by key and only for
 // the keys that a row sees (see the caller).  `init`: O holds nothing yet.
 template <int D, bool kHalf>
-__device__ __noinline__ void add_seen_keys(const AttnParams& a, const int* table, int kvh, int key0, int valid, int lim,
+__device__ __forceinline__ void add_seen_keys(const AttnParams& a, const int* table, int kvh, int key0, int valid, int lim,
                                            uint32_t tS, uint32_t tO, bool init)
 {
+#pragma unroll 1
     for (int half = 0; half < 2; ++half) {
         uint32_t pk[32];
         tmem_ld32(tS + 32u * half, pk);
         tmem_ld_wait(pk);
         uint32_t weight[32];     // indexed at run time: lives in local memory
         for (int c = 0; c < 32; ++c) weight[c] = pk[c];
+#pragma unroll 1
         for (int c4 = 0; c4 < D / 32; ++c4) {
             uint32_t o[32];
             if (!(init && half == 0)) {
@@ -144,6 +151,7 @@ __device__ __noinline__ void add_seen_keys(const AttnParams& a, const int* table
 #pragma unroll
                 for (int c = 0; c < 32; ++c) o[c] = 0u;
             }
+#pragma unroll 1
             for (int k = 0; k < 64 && 64 * half + k < valid; ++k) {
                 const int key = key0 + 64 * half + k;
                 const int pi = page_index(key, a.page_size, a.page_shift), page = table[pi];
@@ -179,6 +187,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long s_scratch[kThreads / 32 + 1];
     __shared__ int s_start[4];             // request, key/value head, tile, key tile
+    __shared__ long long s_offset;         // units into the request
     __shared__ int s_seen[2];              // piece whose O tile u holds sums before its first MMA
     __shared__ int s_odd[2][2];            // check whose V tile holds an infinity or a NaN
     const uint32_t raw_base = smem_u32(smem_raw);
@@ -210,21 +219,32 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     long long mine = 0, total;
     for (int i = i0; i < i1; ++i) mine += Walk::units(p, i);
     const long long before = block_exclusive_sum(mine, s_scratch, &total);
-    const long long share = total / G + (b < total % G);
-    const long long start = total / G * b + min((long long)b, total % G);
+    const Share share = share_of(total, G, b);
+    const long long start = share.start;
     if (tid < 2) p.ws.info[2 * b + tid].req = -1;
-    if (share == 0) return;
+    if (share.count == 0) return;
     if (before <= start && start < before + mine) {
         long long x = start - before;
         int i = i0;
         for (long long c; x >= (c = Walk::units(p, i)); ++i) x -= c;
-        const TileWork w = Walk::work(p, load_request(a, i));
-        const long long head = w.before(w.tiles());
         s_start[0] = i;
-        s_start[1] = (int)(x / head);
-        x %= head;
-        s_start[2] = w.tile_of(x);
-        s_start[3] = (int)(x - w.before(s_start[2]));
+        s_offset = x;
+    }
+    __syncthreads();
+    {
+        // the tile: every thread knows the units before one of kThreads of them
+        const TileWork w = Walk::work(p, load_request(a, s_start[0]));
+        const int count = w.tiles(), each = (count + kThreads - 1) / kThreads;
+        const int lo = min(count, tid * each), hi = min(count, lo + each);
+        const long long head = w.before(count);
+        const int kvh = quotient_below(s_offset, head, a.kv_heads);
+        const long long x = s_offset - kvh * head;
+        if (lo < hi && w.before(lo) <= x && x < w.before(hi)) {
+            const int t = w.tile_of(x, lo, hi);
+            s_start[1] = kvh;
+            s_start[2] = t;
+            s_start[3] = (int)(x - w.before(t));
+        }
     }
 
     WaitCtl wc{abort_flag, a.status, p.wait_limit_ns};
@@ -257,8 +277,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Walk walk(p, s_start[0], s_start[1], s_start[2], s_start[3], share);
+    Walk walk(p, s_start[0], s_start[1], s_start[2], s_start[3], share.count);
 
+    if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
     if (warp == 0) {
         // ------------------------------------------------------------ copies
         const int boxes = kBN / p.box_rows * CF::kBoxes;     // at most 32: one for each lane
@@ -273,7 +295,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         int last_k[CF::kStages], last_v[CF::kStages], last_q = -1;   // parity of the last copy issued
         for (int s = 0; s < CF::kStages; ++s) last_k[s] = last_v[s] = -1;
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+            return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, wc));
         };
         bool ok = true;
         uint32_t n = 0, piece = 0;
@@ -328,10 +350,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             // Let every copy still in flight land before the block exits.
             volatile int dummy = 0;
             WaitCtl drain{&dummy, a.status, 200000000ull};
-            if (last_q >= 0) mbar_wait(bar_q_full, (uint32_t)last_q, drain);
+            if (last_q >= 0) mbar_wait_inline(bar_q_full, (uint32_t)last_q, drain);
             for (int s = 0; s < CF::kStages; ++s) {
-                if (last_k[s] >= 0) mbar_wait(bar_k_full(s), (uint32_t)last_k[s], drain);
-                if (last_v[s] >= 0) mbar_wait(bar_v_full(s), (uint32_t)last_v[s], drain);
+                if (last_k[s] >= 0) mbar_wait_inline(bar_k_full(s), (uint32_t)last_k[s], drain);
+                if (last_v[s] >= 0) mbar_wait_inline(bar_v_full(s), (uint32_t)last_v[s], drain);
             }
         }
         __syncwarp();
@@ -374,7 +396,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             __syncwarp();
         };
         auto wait_all = [&](uint32_t bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc));
+            return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity, wc));
         };
         bool ok = true;
         uint32_t n = 0, piece = 0, done[2] = {0, 0};      // key tiles; pieces; weights of tile u taken
@@ -421,10 +443,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         commit(bar_drain);
         volatile int dummy = 0;
         WaitCtl drain{&dummy, a.status, 200000000ull};
-        __all_sync(0xffffffffu, mbar_wait(bar_drain, 0, drain));
+        __all_sync(0xffffffffu, mbar_wait_inline(bar_drain, 0, drain));
+    }
     } else {
         // ------------------------------------------------- softmax + results
-        const int u = (warp - 2) >> 2;                 // row tile
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        const int u = (warp - 4) >> 2;                 // row tile
         const uint32_t quarter = (uint32_t)(warp & 3); // tensor memory lane quarter
         const int row = (int)quarter * 32 + lane;
         const uint32_t tS = tmem_addr(tmem, quarter * 32, CF::kColS + 128u * u);
@@ -448,7 +472,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             if (u < nu) {
                 for (int kt = walk.k0; kt < k1; ++kt, ++n, ++seen) {
                     // all lanes leave together: the tcgen05 loads below are warp-wide
-                    ok = __all_sync(0xffffffffu, mbar_wait(bar_s_full(u), seen & 1u, wc));
+                    ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_s_full(u), seen & 1u, wc));
                     if (!ok) break;
                     tc_fence_after();
                     uint32_t s[128];
@@ -522,9 +546,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         // never have been written, are cleared; and if a row
                         // in use holds one, all of V is cleared and the keys
                         // are added one by one to the rows that see them.
-                        const int two = nu - 1, group_threads = kBM * nu, me = tid - 64;
+                        const int two = nu - 1, group_threads = kBM * nu, me = tid - 128;
                         const int vs = n % CF::kStages, valid = min(kBN, keys - key0);
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar_v_full(vs), (n / CF::kStages) & 1u, wc));
+                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_v_full(vs), (n / CF::kStages) & 1u, wc));
                         if (!ok) break;
                         const uint32_t v = sV + vs * CF::kTileBytes;
                         volatile int* odd_slot = &s_odd[two][checks[two] & 1u];
@@ -542,7 +566,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         if (odd) *odd_slot = check;
                         fence_proxy_async_smem();
                         mbar_arrive(bar_check(two));
-                        ok = __all_sync(0xffffffffu, mbar_wait(bar_check(two), checks[two] & 1u, wc));
+                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_check(two), checks[two] & 1u, wc));
                         ++checks[two];
                         if (!ok) break;
                         if (*odd_slot == check) {
@@ -550,7 +574,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                                 *reinterpret_cast<uint4*>(gbase + (v - base) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
                             fence_proxy_async_smem();
                             mbar_arrive(bar_check(two));
-                            ok = __all_sync(0xffffffffu, mbar_wait(bar_check(two), checks[two] & 1u, wc));
+                            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_check(two), checks[two] & 1u, wc));
                             ++checks[two];
                             if (!ok) break;
                             add_seen_keys<D, kHalf>(a, a.table + (long long)walk.req * a.table_stride, walk.kvh, key0,
@@ -564,7 +588,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             } else {
                 n += (uint32_t)(k1 - walk.k0);
             }
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(bar_o_final, piece & 1u, wc));
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o_final, piece & 1u, wc));
             if (ok && u < nu) {
                 tc_fence_after();
                 const bool whole = walk.k0 == 0 && k1 == walk.total();

@@ -149,7 +149,7 @@ int main()
                 long long sum = 0;
                 for (int t = 0; t < w.tiles(); ++t) {
                     if (w.before(t) != sum) { std::printf("sum %d %d %d %d\n", q, len, step, t); return 8; }
-                    if (w.tile_of(sum) != t || w.tile_of(sum + w.units(t) - 1) != t) return 9;
+                    if (w.tile_of(sum, 0, w.tiles()) != t || w.tile_of(sum + w.units(t) - 1, t, w.tiles()) != t) return 9;
                     int seen = causal ? len - q + ((t + 1) * step < q ? (t + 1) * step : q) : len;
                     if (seen < 0) seen = 0;
                     if (w.units(t) < 1 || w.units(t) * unit < seen || (w.units(t) > 1 && (w.units(t) - 1) * unit >= seen))
@@ -158,9 +158,24 @@ int main()
                 }
                 if (w.before(w.tiles()) != sum) return 11;
             }
+    for (long long total : {0ll, 1ll, 151ll, 152ll, 153ll, 99999ll, (1ll << 32) + 5, (1ll << 58) + 12345})
+        for (int blocks : {1, 2, 152, 256, 65535}) {
+            long long at = 0;
+            for (int b = 0; b < blocks; ++b) {
+                const Share s = share_of(total, blocks, b);
+                if (s.start != at || s.count < total / blocks || s.count > total / blocks + 1) return 13;
+                at += s.count;
+            }
+            if (at != total) return 14;
+        }
+    for (long long size : {1ll, 7ll, 1ll << 40})
+        for (int count : {1, 2, 8, 1000})
+            for (int x : {0, 1, 6, 7, 500, 999})
+                if (x < count && (quotient_below(x * size, size, count) != x ||
+                                  quotient_below(x * size + size - 1, size, count) != x)) return 15;
     {   // the largest that the calls accept
         const TileWork w{1 << 30, 1 << 30, 1, 1, 16};
-        if (w.before(w.tiles()) <= 0 || w.tile_of(w.before(w.tiles()) - 1) != w.tiles() - 1) return 12;
+        if (w.before(w.tiles()) <= 0 || w.tile_of(w.before(w.tiles()) - 1, 0, w.tiles()) != w.tiles() - 1) return 12;
     }
     // rows past 2^32 elements, and a row behind the last page never named
     const PoolLayout l{8ll * 16 * 128, 128, 16 * 128};
