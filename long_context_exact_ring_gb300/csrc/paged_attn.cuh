@@ -134,7 +134,7 @@ struct PartInfo {
 struct Workspace {
     PartInfo* info;   // [blocks][2]
     float* ml;        // [blocks][2][2][tile rows] reference and sum of the exponentials
-    float* acc;       // [blocks][2][tile rows][D] sums, not normalized
+    float* acc;       // [blocks][2][D / 4][tile rows][4] sums, not normalized
 };
 
 // Workspace of a kernel with tiles of `rows` packed rows.
@@ -150,6 +150,13 @@ __host__ __device__ inline Workspace workspace(void* base, int rows)
     w.ml = reinterpret_cast<float*>(w.info + 2 * kMaxBlocks);
     w.acc = w.ml + (size_t)kMaxBlocks * 2 * 2 * rows;
     return w;
+}
+
+// Where four columns of a part's row lie: the rows of a tile are neighbours, so
+// that lanes which hold a row each write whole lines.
+__device__ __forceinline__ float4* part_columns(const Workspace& ws, int slot, int tile_rows, int D, int row, int col)
+{
+    return reinterpret_cast<float4*>(ws.acc) + ((size_t)slot * (D / 4) + col / 4) * tile_rows + row;
 }
 
 // Which requests a kernel serves: those with more than `above` and at most
@@ -192,7 +199,7 @@ paged_join_kernel(const AttnParams p, const Workspace ws, int blocks, int used, 
     const PartInfo info = ws.info[2 * b + 1];
     if (info.req < 0) return;
     constexpr int kPer = 16 * D / 256;
-    const int row = blockIdx.y * 16 + threadIdx.x / (D / kPer), col = threadIdx.x % (D / kPer) * kPer;
+    const int row = blockIdx.y * 16 + threadIdx.x % 16, col = threadIdx.x / 16 * kPer;
     const Request r = load_request(p, info.req);
     const int packed = info.row0 + row / kHalfRows * used + row % kHalfRows;
     if (row % kHalfRows >= used || packed >= r.q * p.group) return;
@@ -209,10 +216,10 @@ paged_join_kernel(const AttnParams p, const Workspace ws, int blocks, int used, 
         }
         const float mx = ws.ml[(size_t)slot * 2 * kTileRows + row];
         const float lx = ws.ml[(size_t)slot * 2 * kTileRows + kTileRows + row];
-        const float* src = ws.acc + ((size_t)slot * kTileRows + row) * D + col;
         float v[kPer];
 #pragma unroll
-        for (int c = 0; c < kPer; c += 4) *reinterpret_cast<float4*>(v + c) = *reinterpret_cast<const float4*>(src + c);
+        for (int c = 0; c < kPer; c += 4)
+            *reinterpret_cast<float4*>(v + c) = *part_columns(ws, slot, kTileRows, D, row, col + c);
         if (mx != -INFINITY) {
             const float to = max_nan(m, mx), fa = ex2_approx(m - to), fb = ex2_approx(mx - to);
             m = to;
@@ -562,10 +569,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
             if (row < rows) store_row<kPer, kHalf>(p, r, kvh, row0 + row, col, out, m, l, Op::kShift);
         } else {
             const int slot = 2 * b + (u0 == 0);
-            float* dst = ws.acc + ((size_t)slot * kRows + row) * D + col;
 #pragma unroll
             for (int c = 0; c < kPer; c += 4)
-                *reinterpret_cast<float4*>(dst + c) = make_float4(out[c], out[c + 1], out[c + 2], out[c + 3]);
+                *part_columns(ws, slot, kRows, D, row, col + c) = make_float4(out[c], out[c + 1], out[c + 2], out[c + 3]);
             if (col == 0) {
                 ws.ml[slot * 2 * kRows + row] = m;
                 ws.ml[slot * 2 * kRows + kRows + row] = l;

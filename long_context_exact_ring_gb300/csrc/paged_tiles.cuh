@@ -6,8 +6,8 @@
 //   warp 0      copies Q once and K/V tiles page by page (TMA; a page's rows
 //               are boxes of a 4-D tensor map, one lane issues one box)
 //   warp 1      tensor memory and the MMAs: S = Q K^T, O += P V
-//   warps 2-3   nothing: they lend their registers to the warps below, whose
-//               128 scores each would not fit in an even share
+//   warps 2-3   look through V, a half of each tile each, where some row does
+//               not see some key (see below)
 //   warps 4-7   softmax and results of tile 0
 //   warps 8-11  the same of tile 1
 // Tensor memory (512 columns): S0/P0, S1/P1 of 128 columns, then O0, O1.
@@ -101,6 +101,13 @@ struct Walk {
     __device__ __forceinline__ int total() const { return w.units(t); }
     __device__ __forceinline__ int end() const { return (int)min((long long)total(), k0 + left); }
     __device__ __forceinline__ int tok0() const { return t * w.step; }
+    // first key tile of this piece with a key that the block's first row does
+    // not see, or end()
+    __device__ __forceinline__ int first_masked() const
+    {
+        const int last = p.a.causal ? r.len - r.q + tok0() : r.len - 1;
+        return min(end(), max(k0, last < 0 ? 0 : (last + 1) / kBN));
+    }
     // row tiles that hold tokens
     __device__ __forceinline__ int row_tiles() const { return r.q - tok0() > p.tok_tile ? 2 : 1; }
     // To the next piece of work; false behind the last one.
@@ -128,14 +135,14 @@ template <bool kHalf> __device__ __forceinline__ float widen(uint32_t bits)
     else return __uint_as_float(bits << 16);
 }
 
-// O += P V of one key tile for the rows of one warp, key by key and only for
-// the keys that a row sees (see the caller).  `init`: O holds nothing yet.
+// O += P V of one or both halves of a key tile for the rows of one warp, key by
+// key and only for the keys that a row sees.  `init`: O holds nothing yet.
 template <int D, bool kHalf>
 __device__ __forceinline__ void add_seen_keys(const AttnParams& a, const int* table, int kvh, int key0, int valid, int lim,
-                                           uint32_t tS, uint32_t tO, bool init)
+                                              bool lower, bool upper, uint32_t tS, uint32_t tO, bool init)
 {
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
+    for (int half = lower ? 0 : 1; half < (upper ? 2 : 1); ++half) {
         uint32_t pk[32];
         tmem_ld32(tS + 32u * half, pk);
         tmem_ld_wait(pk);
@@ -144,7 +151,7 @@ __device__ __forceinline__ void add_seen_keys(const AttnParams& a, const int* ta
 #pragma unroll 1
         for (int c4 = 0; c4 < D / 32; ++c4) {
             uint32_t o[32];
-            if (!(init && half == 0)) {
+            if (!init || (half == 1 && lower)) {
                 tmem_ld32(tO + 32u * c4, o);
                 tmem_ld_wait(o);
             } else {
@@ -189,7 +196,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     __shared__ int s_start[4];             // request, key/value head, tile, key tile
     __shared__ long long s_offset;         // units into the request
     __shared__ int s_seen[2];              // piece whose O tile u holds sums before its first MMA
-    __shared__ int s_odd[2][2];            // check whose V tile holds an infinity or a NaN
+    __shared__ int s_odd[CF::kStages][2];  // key tile whose V half holds an infinity or a NaN
     const uint32_t raw_base = smem_u32(smem_raw);
     const uint32_t base = (raw_base + 1023u) & ~1023u;
     uint8_t* gbase = smem_raw + (base - raw_base);
@@ -205,7 +212,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     auto bar_p_full = [&](int u) { return bar_misc + 8u * (2 + u); };    // softmax -> MMA
     const uint32_t bar_o_final = bar_misc + 8u * 4;                      // last P V of a piece done
     const uint32_t bar_drain = bar_misc + 8u * 5;
-    auto bar_check = [&](int two) { return bar_misc + 8u * (6 + two); }; // V checked by one or both groups
+    auto bar_check = [&](int s) { return bar_misc + 8u * (6 + s); };     // V looked through
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + CF::kOffBar + 448);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + CF::kOffBar + 456);
 
@@ -223,6 +230,33 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const long long start = share.start;
     if (tid < 2) p.ws.info[2 * b + tid].req = -1;
     if (share.count == 0) return;
+
+    WaitCtl wc{abort_flag, a.status, p.wait_limit_ns};
+    if (tid == 0) {
+        *abort_flag = 0;
+        mbar_init(bar_q_full, 1);
+        mbar_init(bar_q_empty, 1);
+        for (int s = 0; s < CF::kStages; ++s) {
+            mbar_init(bar_k_full(s), 1);
+            mbar_init(bar_k_empty(s), 1);
+            mbar_init(bar_v_full(s), 1);
+            mbar_init(bar_v_empty(s), 3);      // P V and both checking warps
+            mbar_init(bar_check(s), 2);
+            s_odd[s][0] = s_odd[s][1] = 0;
+        }
+        for (int u = 0; u < kTiles; ++u) {
+            mbar_init(bar_s_full(u), 1);
+            mbar_init(bar_p_full(u), kBM);
+            s_seen[u] = 0;
+        }
+        mbar_init(bar_o_final, 1);
+        mbar_init(bar_drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), CF::kTmemCols);
+        tmem_relinquish();
+    }
     if (before <= start && start < before + mine) {
         long long x = start - before;
         int i = i0;
@@ -247,32 +281,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         }
     }
 
-    WaitCtl wc{abort_flag, a.status, p.wait_limit_ns};
-    if (tid == 0) {
-        *abort_flag = 0;
-        mbar_init(bar_q_full, 1);
-        mbar_init(bar_q_empty, 1);
-        for (int s = 0; s < CF::kStages; ++s) {
-            mbar_init(bar_k_full(s), 1);
-            mbar_init(bar_k_empty(s), 1);
-            mbar_init(bar_v_full(s), 1);
-            mbar_init(bar_v_empty(s), 1);
-        }
-        for (int u = 0; u < kTiles; ++u) {
-            mbar_init(bar_s_full(u), 1);
-            mbar_init(bar_p_full(u), kBM);
-            mbar_init(bar_check(u), kBM * (1 + u));
-            s_seen[u] = 0;
-            s_odd[u][0] = s_odd[u][1] = 0;
-        }
-        mbar_init(bar_o_final, 1);
-        mbar_init(bar_drain, 1);
-        fence_mbar_init();
-    }
-    if (warp == 1) {
-        tmem_alloc(smem_u32(tmem_slot), CF::kTmemCols);
-        tmem_relinquish();
-    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -444,6 +452,57 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         volatile int dummy = 0;
         WaitCtl drain{&dummy, a.status, 200000000ull};
         __all_sync(0xffffffffu, mbar_wait_inline(bar_drain, 0, drain));
+    } else {
+        // ------------------------------------------------------------ checks
+        // In a key tile with a key that some row does not see, a weight of 0
+        // does not hide an infinity or a NaN in V.  Rows of V behind the last
+        // key in use, which may never have been written, are cleared; and if a
+        // row in use holds one, this warp's half of V is cleared and the
+        // softmax warps add its keys one by one to the rows that see them.
+        // They see every key tile and hold its V until then, so bar_v_full is
+        // never a phase ahead of them, nor they of it.
+        const int half = warp - 2;
+        bool ok = true;
+        uint32_t n = 0;
+        do {
+            const int k1 = walk.end(), keys = walk.w.keys(walk.t), masked = walk.first_masked();
+            for (int kt = walk.k0; kt < k1; ++kt, ++n) {
+                const int s = n % CF::kStages, valid = keys - kt * kBN;
+                ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_v_full(s), (n / CF::kStages) & 1u, wc));
+                if (!ok) break;
+                if (kt < masked) {
+                    if (lane == 0) mbar_arrive(bar_v_empty(s));
+                    continue;
+                }
+                uint4* v = reinterpret_cast<uint4*>(gbase + CF::kOffV + s * CF::kTileBytes);
+                // a box's rows are 8 pieces of 16 bytes; four rows to a pass
+                const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                bool odd = false;
+                for (int x = 0; x < CF::kBoxes; ++x) {
+                    uint4* at = v + (x * kBN + half * 64) * 8 + lane;
+#pragma unroll 4
+                    for (int y = 0; y < 16; ++y) {
+                        if (half * 64 + 4 * y + (lane >> 3) < valid) {
+                            const uint4 z = at[32 * y];
+                            odd |= Op::nonfinite(z.x) || Op::nonfinite(z.y) || Op::nonfinite(z.z) || Op::nonfinite(z.w);
+                        } else {
+                            at[32 * y] = zero;
+                        }
+                    }
+                }
+                if (__any_sync(0xffffffffu, odd)) {
+                    for (int x = 0; x < CF::kBoxes; ++x)
+                        for (int y = 0; y < 16; ++y) v[(x * kBN + half * 64) * 8 + lane + 32 * y] = zero;
+                    *(volatile int*)&s_odd[s][half] = (int)(n + 1);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar_check(s));
+                    mbar_arrive(bar_v_empty(s));
+                }
+            }
+        } while (ok && walk.next());
     }
     } else {
         // ------------------------------------------------- softmax + results
@@ -456,16 +515,15 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const float sl2 = a.scale_log2;
         const int used = p.tok_tile * a.group;
         bool ok = true;
-        uint32_t n = 0, piece = 0, seen = 0, checks[2] = {0, 0};
+        uint32_t n = 0, piece = 0, seen = 0, looked = 0;    // looked: parities of bar_check
         do {
             const int k1 = walk.end(), nu = walk.row_tiles(), keys = walk.w.keys(walk.t);
             const int packed = walk.tok0() * a.group + u * used + row;
             const int tok = packed / a.group;
             const bool store = row < used && tok < walk.r.q;
-            // last key that the row, the block's first row and the tile's first row see
+            // last key that the row and the tile's first row see
             const int past = walk.r.len - walk.r.q;
             const int lim = a.causal ? past + min(tok, walk.r.q - 1) : walk.r.len - 1;
-            const int lim_block = a.causal ? past + walk.tok0() : walk.r.len - 1;
             const int lim_tile = a.causal ? past + walk.tok0() + u * p.tok_tile : walk.r.len - 1;
             float m_used = -INFINITY;   // reference of the exponentials (log2), without the shift
             float l = 0.f;
@@ -539,46 +597,18 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         }
                     }
                     tmem_st_wait();
-                    if (key0 + kBN - 1 > lim_block) {
-                        // Some row does not see some key of this tile, and a
-                        // weight of 0 does not hide an infinity or a NaN in
-                        // V.  Rows of V behind the last key in use, which may
-                        // never have been written, are cleared; and if a row
-                        // in use holds one, all of V is cleared and the keys
-                        // are added one by one to the rows that see them.
-                        const int two = nu - 1, group_threads = kBM * nu, me = tid - 128;
-                        const int vs = n % CF::kStages, valid = min(kBN, keys - key0);
-                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_v_full(vs), (n / CF::kStages) & 1u, wc));
+                    if (kt >= walk.first_masked()) {
+                        // warps 2-3 have looked through V (see there)
+                        const int vs = n % CF::kStages;
+                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_check(vs), looked >> vs & 1u, wc));
                         if (!ok) break;
-                        const uint32_t v = sV + vs * CF::kTileBytes;
-                        volatile int* odd_slot = &s_odd[two][checks[two] & 1u];
-                        const int check = (int)checks[two] + 1;
-                        bool odd = false;
-                        for (int x = me; x < kBN * D / 8; x += group_threads) {
-                            uint4* at = reinterpret_cast<uint4*>(gbase + (v - base) + x * 16);
-                            if (((x >> 3) & (kBN - 1)) >= valid) {
-                                *at = make_uint4(0u, 0u, 0u, 0u);
-                            } else {
-                                const uint4 y = *at;
-                                odd |= Op::nonfinite(y.x) || Op::nonfinite(y.y) || Op::nonfinite(y.z) || Op::nonfinite(y.w);
-                            }
-                        }
-                        if (odd) *odd_slot = check;
-                        fence_proxy_async_smem();
-                        mbar_arrive(bar_check(two));
-                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_check(two), checks[two] & 1u, wc));
-                        ++checks[two];
-                        if (!ok) break;
-                        if (*odd_slot == check) {
-                            for (int x = me; x < kBN * D / 8; x += group_threads)
-                                *reinterpret_cast<uint4*>(gbase + (v - base) + x * 16) = make_uint4(0u, 0u, 0u, 0u);
-                            fence_proxy_async_smem();
-                            mbar_arrive(bar_check(two));
-                            ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_check(two), checks[two] & 1u, wc));
-                            ++checks[two];
-                            if (!ok) break;
+                        looked ^= 1u << vs;
+                        const int mark = (int)(n + 1);
+                        const bool lower = *(volatile int*)&s_odd[vs][0] == mark;
+                        const bool upper = *(volatile int*)&s_odd[vs][1] == mark;
+                        if (lower || upper) {
                             add_seen_keys<D, kHalf>(a, a.table + (long long)walk.req * a.table_stride, walk.kvh, key0,
-                                                    valid, lim, tS, tO, kt == walk.k0);
+                                                    min(kBN, keys - key0), lim, lower, upper, tS, tO, kt == walk.k0);
                             if (kt == walk.k0) *(volatile int*)&s_seen[u] = (int)(piece + 1);
                         }
                     }
@@ -586,7 +616,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     mbar_arrive(bar_p_full(u));
                 }
             } else {
-                n += (uint32_t)(k1 - walk.k0);
+                n += (uint32_t)(walk.first_masked() - walk.k0);
+                for (int kt = walk.first_masked(); kt < k1; ++kt, ++n) looked ^= 1u << (n % CF::kStages);
             }
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o_final, piece & 1u, wc));
             if (ok && u < nu) {
@@ -618,17 +649,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                             none ? -INFINITY : (m_used - kShift<kHalf> + log2f(l)) * 0.69314718055994531f;
                 } else {
                     const int slot = 2 * b + (walk.k0 == 0);
-                    const size_t prow = (size_t)slot * kTileRows + u * kBM + row;
 #pragma unroll
                     for (int c4 = 0; c4 < D / 32; ++c4) {
                         uint32_t o[32];
                         tmem_ld32(tO + 32u * c4, o);
                         tmem_ld_wait(o);
-                        float4* d4 = reinterpret_cast<float4*>(p.ws.acc + prow * D + 32 * c4);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
-                            d4[x] = make_float4(__uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
-                                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
+                            *part_columns(p.ws, slot, kTileRows, D, u * kBM + row, 32 * c4 + 4 * x) = make_float4(
+                                __uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
+                                __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
                     }
                     // a NaN sum without a maximum (every score NaN) must not read as "no key"
                     float* ml = p.ws.ml + (size_t)slot * 2 * kTileRows + u * kBM + row;
