@@ -91,79 +91,109 @@ int make_paged_map(CUtensorMap* map, const void* ptr, bool half, int d, const in
 
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 
+// A launch that may begin before the kernel in front of it is over
+// (`follows`; see let_next_start).
+template <typename... Params, typename... Args>
+cudaError_t launch_after(bool follows, void (*kernel)(Params...), dim3 grid, int threads, int smem, cudaStream_t s,
+                         Args... args)
+{
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = follows ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Up to 16 packed rows (new tokens x query heads of a key/value head) a
 // request is served by paged_rows_kernel, above by paged_tiles_kernel.
 constexpr int kFewRows = 16;
 
 template <int D, bool kHalf>
-int launch_rows(const ra::paged::AttnParams& p, void* workspace, ra::paged::RowRange range, int blocks, cudaStream_t s)
+cudaError_t launch_rows(const ra::paged::AttnParams& p, const ra::paged::Workspace& ws, ra::paged::RowRange range,
+                        int blocks, cudaStream_t s)
 {
     namespace pr = ra::paged::rows;
-    const int e = allow_smem(pr::paged_rows_kernel<D, kHalf>, pr::Cfg<D>::kSmemBytes);
-    if (e != RA_OK) return e;
-    const ra::paged::Workspace ws = ra::paged::workspace(workspace, pr::kRows);
-    {
-        ra::prof::Scope ps(ra::prof::kPagedRows, s);
-        pr::paged_rows_kernel<D, kHalf><<<blocks, pr::kThreads, pr::Cfg<D>::kSmemBytes, s>>>(p, ws, range);
-        ps.done();
-    }
-    ra::prof::Scope ps(ra::prof::kPagedJoin, s);
-    ra::paged::paged_join_kernel<D, kHalf, pr::kRows, pr::kRows><<<blocks, 256, 0, s>>>(
-        p, ws, blocks, pr::kRows, ra::paged::Operand<kHalf>::kShift);
+    const cudaError_t e = cudaFuncSetAttribute(pr::paged_rows_kernel<D, kHalf>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, pr::Cfg<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ra::prof::Scope ps(ra::prof::kPagedRows, s);
+    const cudaError_t r = launch_after(false, pr::paged_rows_kernel<D, kHalf>, dim3(blocks), pr::kThreads,
+                                       pr::Cfg<D>::kSmemBytes, s, p, ws, range);
     ps.done();
-    const cudaError_t ce = cudaGetLastError();
-    return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged_rows_kernel launch");
+    return r;
+}
+
+// The tensor maps of paged_tiles_kernel.
+struct TileMaps {
+    CUtensorMap q, k, v;
+};
+
+int make_tile_maps(TileMaps* m, const ra::paged::AttnParams& p, bool half, int d, int tok_tile, int box_rows)
+{
+    int rc = make_paged_map(&m->q, p.q, half, d, {p.group, p.tokens, p.kv_heads},
+                            {p.q_head, p.q_tok, p.q_head * p.group}, {p.group, tok_tile, 1});
+    if (rc == RA_OK)
+        rc = make_paged_map(&m->k, p.kc, half, d, {p.page_size, p.kv_heads, p.num_pages}, {p.lk.st, p.lk.sh, p.lk.sp},
+                            {box_rows, 1, 1});
+    if (rc == RA_OK)
+        rc = make_paged_map(&m->v, p.vc, half, d, {p.page_size, p.kv_heads, p.num_pages}, {p.lv.st, p.lv.sh, p.lv.sp},
+                            {box_rows, 1, 1});
+    return rc;
 }
 
 template <int D, bool kHalf>
-int launch_tiles(const ra::paged::AttnParams& p, void* workspace, ra::paged::RowRange range, int blocks,
-                 cudaStream_t s)
+cudaError_t launch_tiles(bool follows, const TileMaps& maps, const ra::paged::tiles::TileParams& p, int blocks,
+                         cudaStream_t s)
 {
     namespace pt = ra::paged::tiles;
-    const int e = allow_smem(pt::paged_tiles_kernel<D, kHalf>, pt::Cfg<D>::kSmemBytes);
-    if (e != RA_OK) return e;
-    pt::TileParams tp;
-    tp.a = p;
-    tp.ws = ra::paged::workspace(workspace, pt::kTileRows);
-    tp.range = range;
-    tp.tok_tile = pt::kBM / p.group;
-    tp.box_rows = std::min(p.page_size & -p.page_size, pt::kBN);
-    tp.wait_limit_ns = g_wait_limit_ns.load();
-    CUtensorMap mq, mk, mv;
-    int rc = make_paged_map(&mq, p.q, kHalf, D, {p.group, p.tokens, p.kv_heads},
-                            {p.q_head, p.q_tok, p.q_head * p.group}, {p.group, tp.tok_tile, 1});
-    if (rc == RA_OK)
-        rc = make_paged_map(&mk, p.kc, kHalf, D, {p.page_size, p.kv_heads, p.num_pages}, {p.lk.st, p.lk.sh, p.lk.sp},
-                            {tp.box_rows, 1, 1});
-    if (rc == RA_OK)
-        rc = make_paged_map(&mv, p.vc, kHalf, D, {p.page_size, p.kv_heads, p.num_pages}, {p.lv.st, p.lv.sh, p.lv.sp},
-                            {tp.box_rows, 1, 1});
-    if (rc != RA_OK) return rc;
-    {
-        ra::prof::Scope ps(ra::prof::kPagedTiles, s);
-        pt::paged_tiles_kernel<D, kHalf><<<blocks, pt::kThreads, pt::Cfg<D>::kSmemBytes, s>>>(mq, mk, mv, tp);
-        ps.done();
-    }
-    ra::prof::Scope ps(ra::prof::kPagedJoin, s);
-    ra::paged::paged_join_kernel<D, kHalf, pt::kTileRows, pt::kBM><<<dim3(blocks, pt::kTileRows / 16), 256, 0, s>>>(
-        p, tp.ws, blocks, tp.tok_tile * p.group, pt::kShift<kHalf>);
+    const cudaError_t e = cudaFuncSetAttribute(pt::paged_tiles_kernel<D, kHalf>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, pt::Cfg<D>::kSmemBytes);
+    if (e != cudaSuccess) return e;
+    ra::prof::Scope ps(ra::prof::kPagedTiles, s);
+    const cudaError_t r = launch_after(follows, pt::paged_tiles_kernel<D, kHalf>, dim3(blocks), pt::kThreads,
+                                       pt::Cfg<D>::kSmemBytes, s, maps.q, maps.k, maps.v, p);
     ps.done();
-    const cudaError_t ce = cudaGetLastError();
-    return ce == cudaSuccess ? (int)RA_OK : fail_cuda(ce, "paged_tiles_kernel launch");
+    return r;
 }
 
 template <int D, bool kHalf>
 int launch_attn(const ra::paged::AttnParams& p, void* workspace, int max_q, int blocks, cudaStream_t s)
 {
-    // Both kernels can serve any request, so a wrong hint costs time only.
-    if ((long long)max_q * p.group <= kFewRows || (long long)p.tokens * p.group <= kFewRows)
-        return launch_rows<D, kHalf>(p, workspace, {0, INT_MAX}, blocks, s);
-    char* tile_space = static_cast<char*>(workspace) + align256(ra::paged::workspace_bytes(ra::paged::rows::kRows, D));
-    if (p.group <= kFewRows) {
-        const int rc = launch_rows<D, kHalf>(p, workspace, {0, kFewRows}, blocks, s);
+    using namespace ra::paged;
+    const Workspace few = ra::paged::workspace(workspace, kRowsTile);
+    const Workspace big = ra::paged::workspace(
+        static_cast<char*>(workspace) + align256(workspace_bytes(kRowsTile, D)), kBigTile);
+    // Both kernels can serve any request, so a wrong hint costs time only: one
+    // kernel alone takes them all where no request should have more rows than
+    // kFewRows, or all should have max_q tokens.
+    bool run_rows = true, run_tiles = true;
+    if ((long long)max_q * p.group <= kFewRows || (long long)p.tokens * p.group <= kFewRows) run_tiles = false;
+    else if (p.group > kFewRows || (long long)p.n * max_q <= p.tokens) run_rows = false;
+    TileMaps maps;
+    tiles::TileParams tp{p, big, {run_rows ? kFewRows : 0, INT_MAX}, tiles::kBM / p.group,
+                         std::min(p.page_size & -p.page_size, tiles::kBN), g_wait_limit_ns.load()};
+    if (run_tiles) {
+        const int rc = make_tile_maps(&maps, p, kHalf, D, tp.tok_tile, tp.box_rows);
         if (rc != RA_OK) return rc;
     }
-    return launch_tiles<D, kHalf>(p, tile_space, {p.group <= kFewRows ? kFewRows : 0, INT_MAX}, blocks, s);
+    cudaError_t e = cudaSuccess;
+    if (run_rows) e = launch_rows<D, kHalf>(p, few, {0, run_tiles ? kFewRows : INT_MAX}, blocks, s);
+    if (run_tiles && e == cudaSuccess) e = launch_tiles<D, kHalf>(run_rows, maps, tp, blocks, s);
+    if (e == cudaSuccess) {
+        const int first = run_tiles ? 0 : kBigSlices, last = run_rows ? kBigSlices + 1 : kBigSlices;
+        ra::prof::Scope ps(ra::prof::kPagedJoin, s);
+        e = launch_after(true, paged_join_kernel<D, kHalf>, dim3(blocks, last - first), 256, 0, s, p, few, big, blocks,
+                         tp.tok_tile * p.group, first);
+        ps.done();
+    }
+    if (e != cudaSuccess) cudaGetLastError();    // reported here, not by a later call
+    return e == cudaSuccess ? (int)RA_OK : fail_cuda(e, "paged attention launch");
 }
 
 }  // namespace

@@ -186,20 +186,26 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Request& r,
             m == -INFINITY ? -INFINITY : (m - shift + log2f(l)) * 0.69314718055994531f;
 }
 
+// Launches that follow one another without a gap: a kernel lets the next one
+// start as soon as SMs are free, and the next one waits, where it needs the
+// results, for the kernels before it to be over.  Every kernel waits at least
+// at its end, so that the last one's end is the end of all.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Joins the parts of a tile that several blocks had a share of: the block
 // that began it, then those behind it, in order -- the sum does not depend
 // on which finished first.  A tile's rows come in halves of kHalfRows, of
-// which the first `used` hold packed rows.  Block (b, y) joins rows 16 y ..
-// 16 y + 15 of the tile that block b began and did not finish.
+// which the first `used` hold packed rows.  Joins rows 16 slice .. 16 slice +
+// 15 of the tile that block b began and did not finish.
 template <int D, bool kHalf, int kTileRows, int kHalfRows>
-__global__ void __launch_bounds__(256)
-paged_join_kernel(const AttnParams p, const Workspace ws, int blocks, int used, float shift)
+__device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& ws, int blocks, int b, int slice,
+                                          int used, float shift)
 {
-    const int b = blockIdx.x;
     const PartInfo info = ws.info[2 * b + 1];
     if (info.req < 0) return;
     constexpr int kPer = 16 * D / 256;
-    const int row = blockIdx.y * 16 + threadIdx.x % 16, col = threadIdx.x / 16 * kPer;
+    const int row = slice * 16 + threadIdx.x % 16, col = threadIdx.x / 16 * kPer;
     const Request r = load_request(p, info.req);
     const int packed = info.row0 + row / kHalfRows * used + row % kHalfRows;
     if (row % kHalfRows >= used || packed >= r.q * p.group) return;
@@ -232,9 +238,28 @@ paged_join_kernel(const AttnParams p, const Workspace ws, int blocks, int used, 
     store_row<kPer, kHalf>(p, r, info.kvh, packed, col, out, m, l, shift);
 }
 
+// The two kernels' tiles (paged_rows_kernel's, paged_tiles_kernel's): rows of
+// a tile, rows of its halves, shift of the reference.
+constexpr int kRowsTile = 16, kBigTile = 256, kBigHalf = 128;
+template <bool kHalf> constexpr float kBigShift = kHalf ? 7.f : 0.f;
+constexpr int kBigSlices = kBigTile / 16;
+
+// Slices 0 .. kBigSlices - 1 of the large tiles, then the small ones.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(256)
+paged_join_kernel(const AttnParams p, const Workspace rows, const Workspace big, int blocks, int used, int first_slice)
+{
+    wait_for_previous();
+    const int slice = blockIdx.y + first_slice;
+    if (slice == kBigSlices)
+        join_part<D, kHalf, kRowsTile, kRowsTile>(p, rows, blocks, blockIdx.x, 0, kRowsTile, Operand<kHalf>::kShift);
+    else
+        join_part<D, kHalf, kBigTile, kBigHalf>(p, big, blocks, blockIdx.x, slice, used, kBigShift<kHalf>);
+}
+
 namespace rows {
 
-constexpr int kRows = 16;        // packed rows of a tile: one m16n8k16 operand
+constexpr int kRows = kRowsTile;   // packed rows of a tile: one m16n8k16 operand
 constexpr int kKeys = 16;        // keys of a warp's step
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
@@ -278,6 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
     const int g = lane >> 2, t4 = lane & 3;
     uint8_t* my = smem_raw + warp * C::kWarpBytes;
     const uint32_t s_my = smem_u32(my);
+    let_next_start();
 
     // ---- this block's share of the work
     auto tiles_of = [&](const Request& r) { return (r.q * p.group + kRows - 1) / kRows; };

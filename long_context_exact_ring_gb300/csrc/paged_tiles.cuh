@@ -29,10 +29,11 @@ namespace ra {
 namespace paged {
 namespace tiles {
 
-constexpr int kBM = 128;           // packed rows of a tile
+constexpr int kBM = kBigHalf;      // packed rows of a tile
 constexpr int kBN = 128;           // keys of a key tile
 constexpr int kTiles = 2;          // row tiles of a block
 constexpr int kTileRows = kTiles * kBM;
+static_assert(kTileRows == kBigTile, "parts are joined as they are cut");
 constexpr int kThreads = 384;
 // Registers of warps 0-3 and of warps 4-11: 128 * 56 + 256 * 224 are the 384 *
 // 168 that the block starts with.
@@ -58,7 +59,7 @@ struct Cfg {
 
 // The weights' reference (see Operand): the running maximum may lag by up to
 // 2^8, so fp16 weights stay below 2^15.
-template <bool kHalf> constexpr float kShift = kHalf ? 7.f : 0.f;
+template <bool kHalf> constexpr float kShift = kBigShift<kHalf>;
 
 struct TileParams {
     AttnParams a;
@@ -218,6 +219,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const AttnParams& a = p.a;
+    let_next_start();
 
     // ---- this block's share of the work
     const int G = gridDim.x, b = blockIdx.x;
@@ -229,7 +231,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const Share share = share_of(total, G, b);
     const long long start = share.start;
     if (tid < 2) p.ws.info[2 * b + tid].req = -1;
-    if (share.count == 0) return;
+    if (share.count == 0) {
+        wait_for_previous();
+        return;
+    }
 
     WaitCtl wc{abort_flag, a.status, p.wait_limit_ns};
     if (tid == 0) {
@@ -679,6 +684,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         tc_fence_after();
         tmem_dealloc(tmem, CF::kTmemCols);
     }
+    // nothing here needs paged_rows_kernel, which may run beside this one
+    wait_for_previous();
 }
 
 }  // namespace tiles
