@@ -17,7 +17,7 @@
 #include "fwd_kernel.cuh"
 #include "bwd_kernel.cuh"
 #include "small_kernels.cuh"
-#include "paged_attn.cuh"
+#include "paged_rows.cuh"
 #include "paged_tiles.cuh"
 
 namespace {
