@@ -108,10 +108,11 @@ RA_HD long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b)
     }
 }
 
-// A request's tiles of `step` new tokens, and the steps of `unit` keys that
-// each takes: those up to the last key its last token sees, at least one.
+// A request's tiles of `step` new tokens and what they cost: the steps of
+// `unit` keys up to the last key that the tile's last token sees, at least
+// one, and `extra` of them for beginning and ending a tile.
 struct TileWork {
-    int q, len, causal, step, unit;
+    int q, len, causal, step, unit, extra;
 
     RA_HD int tiles() const { return (q + step - 1) / step; }
     // keys that tile t's last token sees
@@ -127,21 +128,23 @@ struct TileWork {
         const int k = keys(t);
         return k > 0 ? (k + unit - 1) / unit : 1;
     }
-    // units of the tiles before t, 0 <= t <= tiles()
+    // cost of the tiles before t, 0 <= t <= tiles()
     RA_HD long long before(int t) const
     {
         if (t <= 0) return 0;
-        if (!causal) return (long long)t * units(0);
+        long long sum = (long long)t * extra;
+        if (!causal) return sum + (long long)t * units(0);
         // the last tile may be short: it comes on top
-        const int last = t == tiles() ? units(--t) : 0;
+        if (t == tiles()) sum += units(--t);
         // tiles 0 .. t-1 end at token (i + 1) step: units 1 + (first + i step) / unit
         // from the first tile on that sees a key
         const int first = len - q + step - 1;
         const int blind = first < 0 ? (-first + step - 1) / step : 0;
-        if (t <= blind) return t + last;
-        return t + last + floor_sum((unsigned)(t - blind), (unsigned)unit, (unsigned)step, (unsigned)(first + blind * step));
+        sum += t;
+        if (t <= blind) return sum;
+        return sum + floor_sum((unsigned)(t - blind), (unsigned)unit, (unsigned)step, (unsigned)(first + blind * step));
     }
-    // the tile that unit x lies in, out of tiles [lo, hi), before(lo) <= x < before(hi)
+    // the tile that cost x lies in, out of tiles [lo, hi), before(lo) <= x < before(hi)
     RA_HD int tile_of(long long x, int lo, int hi) const
     {
         while (hi - lo > 1) {
@@ -152,6 +155,11 @@ struct TileWork {
         return lo;
     }
 };
+
+// Where a share's end at cost `c` cuts a tile: the steps of keys in front of
+// it.  A tile's extra cost comes first, so a cut inside it is one in front of
+// the tile.
+RA_HD int cut_units(long long c, int extra) { return c > extra ? (int)(c - extra) : 0; }
 
 }  // namespace paged
 }  // namespace ra

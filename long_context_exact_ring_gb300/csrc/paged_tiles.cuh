@@ -70,24 +70,31 @@ struct TileParams {
     uint64_t wait_limit_ns;
 };
 
-// A block's place in its share.
+// What a tile costs beside its key tiles, in key tiles: Q has to arrive, the
+// pipeline to fill and to drain, and the results to be written, 5 to 6 us
+// against 1.5 to 1.7 us for a key tile.  40 requests with 5 chunks of up to 1024
+// tokens, d 64: 319 us without it, 254 with 2, 241 with 3 or 4, 254 with 6.
+constexpr int kExtra = 3;
+
+// A block's place in its share: key tiles [k0, k1) of a tile, of `total`.
 struct Walk {
     const TileParams& p;
     Request r;
     TileWork w;
-    int req, kvh, t, k0;
-    long long left;
+    int req, kvh, t, k0, k1, total;
+    long long left;          // cost of what follows this piece
 
-    __device__ __forceinline__ Walk(const TileParams& p_, int req_, int kvh_, int t_, int k0_, long long left_)
-        : p(p_), req(req_), kvh(kvh_), t(t_), k0(k0_), left(left_)
+    __device__ __forceinline__ Walk(const TileParams& p_, int req_, int kvh_, int t_, long long c0, long long share)
+        : p(p_), req(req_), kvh(kvh_), t(t_), left(share)
     {
         load();
+        cut(c0);
     }
     static __device__ __forceinline__ TileWork work(const TileParams& p, const Request& r)
     {
-        return TileWork{r.q, r.len, p.a.causal, kTiles * p.tok_tile, kBN};
+        return TileWork{r.q, r.len, p.a.causal, kTiles * p.tok_tile, kBN, kExtra};
     }
-    static __device__ __forceinline__ long long units(const TileParams& p, int i)
+    static __device__ __forceinline__ long long cost(const TileParams& p, int i)
     {
         const Request r = load_request(p.a, i);
         if (!p.range.has(r.q * p.a.group)) return 0;
@@ -99,33 +106,43 @@ struct Walk {
         r = load_request(p.a, req);
         w = work(p, r);
     }
-    __device__ __forceinline__ int total() const { return w.units(t); }
-    __device__ __forceinline__ int end() const { return (int)min((long long)total(), k0 + left); }
+    // The piece that begins at cost c0 of the tile.
+    __device__ __forceinline__ void cut(long long c0)
+    {
+        total = w.units(t);
+        const long long c1 = min((long long)total + kExtra, c0 + left);
+        left -= c1 - c0;
+        k0 = cut_units(c0, kExtra);
+        k1 = cut_units(c1, kExtra);
+    }
+    // The share ends in front of the tile's first key tile.
+    __device__ __forceinline__ bool empty() const { return k0 == k1; }
     __device__ __forceinline__ int tok0() const { return t * w.step; }
     // first key tile of this piece with a key that the block's first row does
-    // not see, or end()
+    // not see, or k1
     __device__ __forceinline__ int first_masked() const
     {
         const int last = p.a.causal ? r.len - r.q + tok0() : r.len - 1;
-        return min(end(), max(k0, last < 0 ? 0 : (last + 1) / kBN));
+        return min(k1, max(k0, last < 0 ? 0 : (last + 1) / kBN));
     }
     // row tiles that hold tokens
     __device__ __forceinline__ int row_tiles() const { return r.q - tok0() > p.tok_tile ? 2 : 1; }
     // To the next piece of work; false behind the last one.
     __device__ __forceinline__ bool next()
     {
-        left -= end() - k0;
         if (left == 0) return false;
-        k0 = 0;
-        if (++t < w.tiles()) return true;
-        t = 0;
-        if (++kvh < p.a.kv_heads) return true;
-        kvh = 0;
-        do {
-            ++req;
-            load();
-        } while (!p.range.has(r.q * p.a.group));    // some later request has the work that is left
-        return true;
+        if (++t == w.tiles()) {
+            t = 0;
+            if (++kvh == p.a.kv_heads) {
+                kvh = 0;
+                do {
+                    ++req;
+                    load();
+                } while (!p.range.has(r.q * p.a.group));    // some later request has the work that is left
+            }
+        }
+        cut(0);
+        return !empty();
     }
 };
 
@@ -194,8 +211,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     using Op = Operand<kHalf>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long s_scratch[kThreads / 32 + 1];
-    __shared__ int s_start[4];             // request, key/value head, tile, key tile
-    __shared__ long long s_offset;         // units into the request
+    __shared__ int s_start[3];             // request, key/value head, tile
+    __shared__ long long s_offset, s_cost; // cost in front of the share, into the request and the tile
     __shared__ int s_seen[2];              // piece whose O tile u holds sums before its first MMA
     __shared__ int s_odd[CF::kStages][2];  // key tile whose V half holds an infinity or a NaN
     const uint32_t raw_base = smem_u32(smem_raw);
@@ -226,7 +243,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const int per = (a.n + kThreads - 1) / kThreads;
     const int i0 = min(a.n, tid * per), i1 = min(a.n, i0 + per);
     long long mine = 0, total;
-    for (int i = i0; i < i1; ++i) mine += Walk::units(p, i);
+    for (int i = i0; i < i1; ++i) mine += Walk::cost(p, i);
     const long long before = block_exclusive_sum(mine, s_scratch, &total);
     const Share share = share_of(total, G, b);
     const long long start = share.start;
@@ -265,13 +282,13 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     if (before <= start && start < before + mine) {
         long long x = start - before;
         int i = i0;
-        for (long long c; x >= (c = Walk::units(p, i)); ++i) x -= c;
+        for (long long c; x >= (c = Walk::cost(p, i)); ++i) x -= c;
         s_start[0] = i;
         s_offset = x;
     }
     __syncthreads();
     {
-        // the tile: every thread knows the units before one of kThreads of them
+        // the tile: every thread knows the cost before one of kThreads of them
         const TileWork w = Walk::work(p, load_request(a, s_start[0]));
         const int count = w.tiles(), each = (count + kThreads - 1) / kThreads;
         const int lo = min(count, tid * each), hi = min(count, lo + each);
@@ -282,7 +299,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             const int t = w.tile_of(x, lo, hi);
             s_start[1] = kvh;
             s_start[2] = t;
-            s_start[3] = (int)(x - w.before(t));
+            s_cost = x - w.before(t);
         }
     }
 
@@ -290,7 +307,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    Walk walk(p, s_start[0], s_start[1], s_start[2], s_start[3], share.count);
+    Walk walk(p, s_start[0], s_start[1], s_start[2], s_cost, share.count);
+    const bool any = !walk.empty();
 
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -312,9 +330,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         };
         bool ok = true;
         uint32_t n = 0, piece = 0;
-        do {
+        if (any) do {
             const int* table = a.table + (long long)walk.req * a.table_stride;
-            const int keys = walk.w.keys(walk.t), k1 = walk.end(), nu = walk.row_tiles();
+            const int keys = walk.w.keys(walk.t), k1 = walk.k1, nu = walk.row_tiles();
             auto page_at = [&](int kt) {
                 const int key = kt * kBN + box * p.box_rows;
                 return lane < boxes && kt < k1 && key < keys
@@ -413,8 +431,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         };
         bool ok = true;
         uint32_t n = 0, piece = 0, done[2] = {0, 0};      // key tiles; pieces; weights of tile u taken
-        do {
-            const int count = walk.end() - walk.k0, nu = walk.row_tiles();
+        if (any) do {
+            const int count = walk.k1 - walk.k0, nu = walk.row_tiles();
             const int s0 = n % CF::kStages;
             if (!(ok = wait_all(bar_q_full, piece & 1u) && wait_all(bar_k_full(s0), (n / CF::kStages) & 1u))) break;
             tc_fence_after();
@@ -469,8 +487,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int half = warp - 2;
         bool ok = true;
         uint32_t n = 0;
-        do {
-            const int k1 = walk.end(), keys = walk.w.keys(walk.t), masked = walk.first_masked();
+        if (any) do {
+            const int k1 = walk.k1, keys = walk.w.keys(walk.t), masked = walk.first_masked();
             for (int kt = walk.k0; kt < k1; ++kt, ++n) {
                 const int s = n % CF::kStages, valid = keys - kt * kBN;
                 ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_v_full(s), (n / CF::kStages) & 1u, wc));
@@ -521,8 +539,8 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const int used = p.tok_tile * a.group;
         bool ok = true;
         uint32_t n = 0, piece = 0, seen = 0, looked = 0;    // looked: parities of bar_check
-        do {
-            const int k1 = walk.end(), nu = walk.row_tiles(), keys = walk.w.keys(walk.t);
+        if (any) do {
+            const int k1 = walk.k1, nu = walk.row_tiles(), keys = walk.w.keys(walk.t);
             const int packed = walk.tok0() * a.group + u * used + row;
             const int tok = packed / a.group;
             const bool store = row < used && tok < walk.r.q;
@@ -627,7 +645,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o_final, piece & 1u, wc));
             if (ok && u < nu) {
                 tc_fence_after();
-                const bool whole = walk.k0 == 0 && k1 == walk.total();
+                const bool whole = walk.k0 == 0 && k1 == walk.total;
                 if (whole) {
                     const bool none = m_used == -INFINITY && l == 0.f;    // no key with a weight
                     const float inv = none ? 0.f : 1.f / l;
@@ -670,7 +688,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     ml[0] = l == l ? m_used : l;
                     ml[kTileRows] = l;
                     if (row == 0 && u == 0)
-                        p.ws.info[slot] = PartInfo{walk.req, walk.kvh, walk.tok0() * a.group, k1 == walk.total()};
+                        p.ws.info[slot] = PartInfo{walk.req, walk.kvh, walk.tok0() * a.group, k1 == walk.total};
                 }
             }
             ++piece;

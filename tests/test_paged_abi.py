@@ -145,16 +145,16 @@ int main()
     for (int q : {1, 31, 32, 33, 64, 100, 509, 1500})
         for (int len : {0, 1, 5, 63, 64, 65, 128, 500, 509, 512, 4096, 131072})
             for (int causal : {0, 1}) for (int step : {1, 2, 36, 64, 256}) for (int unit : {16, 128}) {
-                const TileWork w{q, len, causal, step, unit};
+                const TileWork w{q, len, causal, step, unit, unit == 16 ? 0 : 3};
                 long long sum = 0;
                 for (int t = 0; t < w.tiles(); ++t) {
                     if (w.before(t) != sum) { std::printf("sum %d %d %d %d\n", q, len, step, t); return 8; }
-                    if (w.tile_of(sum, 0, w.tiles()) != t || w.tile_of(sum + w.units(t) - 1, t, w.tiles()) != t) return 9;
+                    if (w.tile_of(sum, 0, w.tiles()) != t || w.tile_of(sum + w.units(t) + w.extra - 1, t, w.tiles()) != t) return 9;
                     int seen = causal ? len - q + ((t + 1) * step < q ? (t + 1) * step : q) : len;
                     if (seen < 0) seen = 0;
                     if (w.units(t) < 1 || w.units(t) * unit < seen || (w.units(t) > 1 && (w.units(t) - 1) * unit >= seen))
                         return 10;
-                    sum += w.units(t);
+                    sum += w.units(t) + w.extra;
                 }
                 if (w.before(w.tiles()) != sum) return 11;
             }
@@ -173,8 +173,9 @@ int main()
             for (int x : {0, 1, 6, 7, 500, 999})
                 if (x < count && (quotient_below(x * size, size, count) != x ||
                                   quotient_below(x * size + size - 1, size, count) != x)) return 15;
+    if (cut_units(0, 3) != 0 || cut_units(3, 3) != 0 || cut_units(4, 3) != 1 || cut_units(7, 0) != 7) return 16;
     {   // the largest that the calls accept
-        const TileWork w{1 << 30, 1 << 30, 1, 1, 16};
+        const TileWork w{1 << 30, 1 << 30, 1, 1, 16, 3};
         if (w.before(w.tiles()) <= 0 || w.tile_of(w.before(w.tiles()) - 1, 0, w.tiles()) != w.tiles() - 1) return 12;
     }
     // rows past 2^32 elements, and a row behind the last page never named
