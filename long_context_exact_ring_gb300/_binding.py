@@ -72,6 +72,8 @@ class RingAttnError(RuntimeError):
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load libringattn.so (raises OSError if it is absent)."""
     global _lib
+    if _lib is not None and path is None:
+        return _lib
     with _lock:
         if _lib is not None and path is None:
             return _lib

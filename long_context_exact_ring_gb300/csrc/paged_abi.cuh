@@ -56,13 +56,30 @@ int page_shift(int page_size)
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
-// Once per device, before the first launch of a kernel with this much
-// dynamic shared memory.
-template <typename Kernel>
-int allow_smem(Kernel kernel, int bytes)
+template <int D, bool kHalf>
+cudaError_t configure_attn_kernels()
 {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    return e == cudaSuccess ? RA_OK : fail_cuda(e, "cudaFuncSetAttribute");
+    cudaError_t e = cudaFuncSetAttribute(ra::paged::rows::paged_rows_kernel<D, kHalf>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         ra::paged::rows::Cfg<D>::kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ra::paged::tiles::paged_tiles_kernel<D, kHalf>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, ra::paged::tiles::Cfg<D>::kSmemBytes);
+    return e;
+}
+
+// Shared-memory and cluster limits of the kernels, once per device.
+cudaError_t configure_paged_kernels()
+{
+    cudaError_t e = cudaFuncSetAttribute(ra::paged::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)ra::paged::plan_smem(ra::paged::kMaxRequests));
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(ra::paged::paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) e = configure_attn_kernels<64, false>();
+    if (e == cudaSuccess) e = configure_attn_kernels<64, true>();
+    if (e == cudaSuccess) e = configure_attn_kernels<128, false>();
+    if (e == cudaSuccess) e = configure_attn_kernels<128, true>();
+    return e;
 }
 
 // 4-D tiled map of 2-byte elements with 128-byte swizzle, 64 columns wide.
@@ -119,9 +136,6 @@ cudaError_t launch_rows(const ra::paged::AttnParams& p, const ra::paged::Workspa
                         int blocks, cudaStream_t s)
 {
     namespace pr = ra::paged::rows;
-    const cudaError_t e = cudaFuncSetAttribute(pr::paged_rows_kernel<D, kHalf>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, pr::Cfg<D>::kSmemBytes);
-    if (e != cudaSuccess) return e;
     ra::prof::Scope ps(ra::prof::kPagedRows, s);
     const cudaError_t r = launch_after(false, pr::paged_rows_kernel<D, kHalf>, dim3(blocks), pr::kThreads,
                                        pr::Cfg<D>::kSmemBytes, s, p, ws, range);
@@ -152,9 +166,6 @@ cudaError_t launch_tiles(bool follows, const TileMaps& maps, const ra::paged::ti
                          cudaStream_t s)
 {
     namespace pt = ra::paged::tiles;
-    const cudaError_t e = cudaFuncSetAttribute(pt::paged_tiles_kernel<D, kHalf>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, pt::Cfg<D>::kSmemBytes);
-    if (e != cudaSuccess) return e;
     ra::prof::Scope ps(ra::prof::kPagedTiles, s);
     const cudaError_t r = launch_after(follows, pt::paged_tiles_kernel<D, kHalf>, dim3(blocks), pt::kThreads,
                                        pt::Cfg<D>::kSmemBytes, s, maps.q, maps.k, maps.v, p);
@@ -226,13 +237,9 @@ int paged_kv_plan(const int* seq_lens, const int* new_lens, int n, int* block_ta
                             page_shift(page_size), tokens};
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const size_t smem = ra::paged::plan_smem(n);
-    if (smem > 48 * 1024) {
-        e = allow_smem(ra::paged::paged_plan_kernel, (int)ra::paged::plan_smem(ra::paged::kMaxRequests));
-        if (e != RA_OK) return e;
-    }
     const unsigned blocks = ra::paged::kPlanCluster;
-    cudaError_t ce = cudaFuncSetAttribute(ra::paged::paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (ce == cudaSuccess) {
+    cudaError_t ce;
+    {
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
         attr.val.clusterDim.x = blocks;

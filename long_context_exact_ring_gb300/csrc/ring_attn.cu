@@ -50,6 +50,8 @@ int fail_cuda(cudaError_t e, const char* what)
     return RA_ERR_CUDA;
 }
 
+cudaError_t configure_paged_kernels();   // paged_abi.cuh
+
 // Per-device set-up, once per device: resolve the status word's device
 // address, raise the kernels' shared-memory limits, find the TMA encoder.
 int device_state(DeviceState** out)
@@ -91,6 +93,7 @@ int device_state(DeviceState** out)
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      ra::fwd::Cfg<128>::kSmemBytes);
         if (e == cudaSuccess) e = ra::bwd::configure_kernels();
+        if (e == cudaSuccess) e = configure_paged_kernels();
         if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute");
         st.ready = true;
     }
