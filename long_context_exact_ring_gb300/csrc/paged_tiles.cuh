@@ -10,9 +10,13 @@
 //               not see some key (see below)
 //   warps 4-7   softmax and results of tile 0
 //   warps 8-11  the same of tile 1
-// Tensor memory (512 columns): S0/P0, S1/P1 of 128 columns, then O0, O1.
-// P, rounded to the operand type (half a step of 2^-9 or 2^-12 each; the row
-// sums take it unrounded), overwrites the first 64 columns of its S.
+// Tensor memory (512 columns): S0, S1 of 128 columns, then O0, O1.  P, rounded
+// to the operand type (half a step of 2^-9 or 2^-12 each; the row sums take it
+// unrounded), overwrites the first 64 columns of its S, so the next S comes
+// behind P V.  With d 64 there is room for P of its own, and the next S is
+// computed while the softmax of this one runs: OWNP_NOTE.
+// (Two S of 64 keys instead, which d 128 has room for, are slower: 2.90 us a key
+// tile against 1.73, as the hand-offs between the warps double.)
 //
 // The work is cut into equal, contiguous shares of (request, key/value head,
 // tile, key tile), one for each SM: with as few tiles as a single chunk of a
@@ -55,6 +59,9 @@ struct Cfg {
     static constexpr uint32_t kTmemCols = 512;
     static constexpr uint32_t kColS = 0;          // S_u at kColS + 128 u
     static constexpr uint32_t kColO = 256;        // O_u at kColO + D u
+    static constexpr bool kOwnP = D == 64;
+    static constexpr uint32_t kColP = kOwnP ? kColO + 2 * D : kColS;      // P_u at kColP + kPitchP u
+    static constexpr uint32_t kPitchP = kOwnP ? 64 : 128;
 };
 
 // The weights' reference (see Operand): the running maximum may lag by up to
@@ -228,9 +235,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const uint32_t bar_misc = bar0 + 8u * (2 + 4 * CF::kStages);
     auto bar_s_full = [&](int u) { return bar_misc + 8u * u; };          // MMA -> softmax
     auto bar_p_full = [&](int u) { return bar_misc + 8u * (2 + u); };    // softmax -> MMA
-    const uint32_t bar_o_final = bar_misc + 8u * 4;                      // last P V of a piece done
-    const uint32_t bar_drain = bar_misc + 8u * 5;
-    auto bar_check = [&](int s) { return bar_misc + 8u * (6 + s); };     // V looked through
+    auto bar_o = [&](int u) { return bar_misc + 8u * (4 + u); };         // P V done: each (own P), or a piece's last
+    auto bar_s_taken = [&](int u) { return bar_misc + 8u * (6 + u); };   // softmax -> MMA: S read (own P)
+    const uint32_t bar_drain = bar_misc + 8u * 8;
+    auto bar_check = [&](int s) { return bar_misc + 8u * (9 + s); };     // V looked through
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + CF::kOffBar + 448);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(gbase + CF::kOffBar + 456);
 
@@ -269,9 +277,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         for (int u = 0; u < kTiles; ++u) {
             mbar_init(bar_s_full(u), 1);
             mbar_init(bar_p_full(u), kBM);
+            mbar_init(bar_o(u), 1);
+            mbar_init(bar_s_taken(u), kBM);
             s_seen[u] = 0;
         }
-        mbar_init(bar_o_final, 1);
         mbar_init(bar_drain, 1);
         fence_mbar_init();
     }
@@ -417,7 +426,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < kBN / 16; ++kk)
-                    mma_bf16_ts(tmem + CF::kColO + (uint32_t)D * u, tmem + CF::kColS + 128u * u + 8u * kk,
+                    mma_bf16_ts(tmem + CF::kColO + (uint32_t)D * u, tmem + CF::kColP + CF::kPitchP * u + 8u * kk,
                                 dv + (uint32_t)kk * (2048 >> 4), idesc_pv, (first && kk == 0) ? 0u : 1u);
             }
             __syncwarp();
@@ -431,6 +440,47 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         };
         bool ok = true;
         uint32_t n = 0, piece = 0, done[2] = {0, 0};      // key tiles; pieces; weights of tile u taken
+        if constexpr (CF::kOwnP) {
+            // S of the next key tile as soon as both softmax groups have read
+            // this one's, then P V of this one.
+            uint32_t issued[2] = {0, 0};                  // S of tile u
+            auto next_s = [&](int nu, int s) {
+                for (int u = 0; u < nu; ++u) {
+                    if (issued[u] > 0 && !wait_all(bar_s_taken(u), (issued[u] - 1) & 1u)) return false;
+                    ++issued[u];
+                    tc_fence_after();
+                    issue_s(u, s);
+                    commit(bar_s_full(u));
+                }
+                commit(bar_k_empty(s));
+                return true;
+            };
+            if (any) do {
+                const int count = walk.k1 - walk.k0, nu = walk.row_tiles();
+                const int s0 = n % CF::kStages;
+                if (!(ok = wait_all(bar_q_full, piece & 1u) && wait_all(bar_k_full(s0), (n / CF::kStages) & 1u))) break;
+                tc_fence_after();
+                if (!(ok = next_s(nu, s0))) break;
+                if (count == 1) commit(bar_q_empty);
+                for (int j = 0; j < count && ok; ++j, ++n) {
+                    const int s = n % CF::kStages, s1 = (n + 1) % CF::kStages;
+                    if (j + 1 < count) {
+                        if (!(ok = wait_all(bar_k_full(s1), ((n + 1) / CF::kStages) & 1u) && next_s(nu, s1))) break;
+                        if (j + 2 == count) commit(bar_q_empty);
+                    }
+                    if (!(ok = wait_all(bar_v_full(s), (n / CF::kStages) & 1u))) break;
+                    for (int u = 0; u < nu; ++u) {
+                        if (!(ok = wait_all(bar_p_full(u), done[u] & 1u))) break;
+                        ++done[u];
+                        tc_fence_after();
+                        issue_pv(u, s, j == 0 && *(volatile int*)&s_seen[u] != (int)(piece + 1));
+                        commit(bar_o(u));
+                    }
+                    if (ok) commit(bar_v_empty(s));
+                }
+                ++piece;
+            } while (ok && walk.next());
+        } else
         if (any) do {
             const int count = walk.k1 - walk.k0, nu = walk.row_tiles();
             const int s0 = n % CF::kStages;
@@ -452,6 +502,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     tc_fence_after();
                     const bool first = j == 0 && *(volatile int*)&s_seen[u] != (int)(piece + 1);
                     issue_pv(u, s, first);
+                    if (!more) commit(bar_o(u));
                     if (u == nu - 1) commit(bar_v_empty(s));
                     if (more) {
                         if (u == 0) {
@@ -467,7 +518,6 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     }
                 }
             }
-            if (ok) commit(bar_o_final);
             ++piece;
         } while (ok && walk.next());
         // Every MMA issued so far must finish before tensor memory is released.
@@ -534,11 +584,12 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t quarter = (uint32_t)(warp & 3); // tensor memory lane quarter
         const int row = (int)quarter * 32 + lane;
         const uint32_t tS = tmem_addr(tmem, quarter * 32, CF::kColS + 128u * u);
+        const uint32_t tP = tmem_addr(tmem, quarter * 32, CF::kColP + CF::kPitchP * u);
         const uint32_t tO = tmem_addr(tmem, quarter * 32, CF::kColO + (uint32_t)D * u);
         const float sl2 = a.scale_log2;
         const int used = p.tok_tile * a.group;
         bool ok = true;
-        uint32_t n = 0, piece = 0, seen = 0, looked = 0;    // looked: parities of bar_check
+        uint32_t n = 0, piece = 0, seen = 0, outs = 0, looked = 0;    // looked: parities of bar_check
         if (any) do {
             const int k1 = walk.k1, nu = walk.row_tiles(), keys = walk.w.keys(walk.t);
             const int packed = walk.tok0() * a.group + u * used + row;
@@ -564,6 +615,10 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[32]));
                     tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[64]));
                     tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(&s[96]));
+                    if constexpr (CF::kOwnP) {
+                        tc_fence_before();
+                        mbar_arrive(bar_s_taken(u));
+                    }
                     const int key0 = kt * kBN;
                     if (key0 + kBN - 1 > lim_tile) {
                         const int last = lim - key0;
@@ -603,12 +658,19 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         sp[2 * x + 1] += p1;
                         s[c >> 1] = Op::pack(p0, p1);
                     }
-                    tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(&s[0]));
-                    tmem_st32(tS + 32u, *reinterpret_cast<const uint32_t(*)[32]>(&s[32]));
+                    if (CF::kOwnP && kt > walk.k0) {
+                        // the P V before this one has read P, and left O
+                        ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o(u), outs & 1u, wc));
+                        if (!ok) break;
+                        ++outs;
+                        tc_fence_after();
+                    }
+                    tmem_st32(tP, *reinterpret_cast<const uint32_t(*)[32]>(&s[0]));
+                    tmem_st32(tP + 32u, *reinterpret_cast<const uint32_t(*)[32]>(&s[32]));
                     l = l * alpha + ((sp[0] + sp[1]) + (sp[2] + sp[3]));
                     if (kt > walk.k0 && __any_sync(0xffffffffu, raise)) {
-                        // O_u is idle: the S_u just read was issued after the last
-                        // P_u V, and its completion covers every earlier MMA.
+                        // O_u is idle: without its own P, the S_u just read was issued
+                        // after the last P_u V and its end covers every earlier MMA.
 #pragma unroll
                         for (int c4 = 0; c4 < D / 32; ++c4) {
                             uint32_t o[32];
@@ -631,7 +693,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         const bool upper = *(volatile int*)&s_odd[vs][1] == mark;
                         if (lower || upper) {
                             add_seen_keys<D, kHalf>(a, a.table + (long long)walk.req * a.table_stride, walk.kvh, key0,
-                                                    min(kBN, keys - key0), lim, lower, upper, tS, tO, kt == walk.k0);
+                                                    min(kBN, keys - key0), lim, lower, upper, tP, tO, kt == walk.k0);
                             if (kt == walk.k0) *(volatile int*)&s_seen[u] = (int)(piece + 1);
                         }
                     }
@@ -642,7 +704,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 n += (uint32_t)(walk.first_masked() - walk.k0);
                 for (int kt = walk.first_masked(); kt < k1; ++kt, ++n) looked ^= 1u << (n % CF::kStages);
             }
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o_final, piece & 1u, wc));
+            if (ok && u < nu) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o(u), outs++ & 1u, wc));
             if (ok && u < nu) {
                 tc_fence_after();
                 const bool whole = walk.k0 == 0 && k1 == walk.total;
