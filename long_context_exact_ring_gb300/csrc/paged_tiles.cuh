@@ -27,6 +27,8 @@
 // of one key/value head read its keys at about the same time, from L2.
 #pragma once
 
+#include <new>
+
 #include "paged_attn.cuh"
 
 namespace ra {
@@ -39,9 +41,9 @@ constexpr int kTiles = 2;          // row tiles of a block
 constexpr int kTileRows = kTiles * kBM;
 static_assert(kTileRows == kBigTile, "parts are joined as they are cut");
 constexpr int kThreads = 384;
-// Registers of warps 0-3 and of warps 4-11: 128 * 56 + 256 * 224 are the 384 *
+// Registers of warps 0-3 and of warps 4-11: 128 * 104 + 256 * 200 are the 384 *
 // 168 that the block starts with.
-constexpr int kFewRegs = 88, kManyRegs = 208;
+constexpr int kFewRegs = 104, kManyRegs = 200;
 constexpr float kRescaleThreshold = 8.0f;   // log2 units
 
 template <int D>
@@ -318,6 +320,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     const uint32_t tmem = *tmem_slot;
     Walk walk(p, s_start[0], s_start[1], s_start[2], s_cost, share.count);
     const bool any = !walk.empty();
+    // The softmax warps keep theirs in shared memory: with 128 scores in
+    // registers there is no room for it beside them.
+    __shared__ __align__(16) uint8_t s_walk[8][sizeof(Walk)];
 
     if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
@@ -588,10 +593,14 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
         const uint32_t tO = tmem_addr(tmem, quarter * 32, CF::kColO + (uint32_t)D * u);
         const float sl2 = a.scale_log2;
         const int used = p.tok_tile * a.group;
-        bool ok = true;
+        Walk* const place = reinterpret_cast<Walk*>(s_walk[warp - 4]);
+        if (lane == 0) new (place) Walk(walk);
+        __syncwarp();
+        bool ok = true, more = any;
         uint32_t n = 0, piece = 0, seen = 0, outs = 0, looked = 0;    // looked: parities of bar_check
-        if (any) do {
-            const int k1 = walk.k1, nu = walk.row_tiles(), keys = walk.w.keys(walk.t);
+        while (ok && more) {
+            const Walk& walk = *place;
+            const int k0 = walk.k0, k1 = walk.k1, nu = walk.row_tiles(), masked = walk.first_masked();
             const int packed = walk.tok0() * a.group + u * used + row;
             const int tok = packed / a.group;
             const bool store = row < used && tok < walk.r.q;
@@ -602,7 +611,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
             float m_used = -INFINITY;   // reference of the exponentials (log2), without the shift
             float l = 0.f;
             if (u < nu) {
-                for (int kt = walk.k0; kt < k1; ++kt, ++n, ++seen) {
+                for (int kt = k0; kt < k1; ++kt, ++n, ++seen) {
                     // all lanes leave together: the tcgen05 loads below are warp-wide
                     ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_s_full(u), seen & 1u, wc));
                     if (!ok) break;
@@ -651,14 +660,15 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     float sp[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int c = 0; c < 128; c += 2) {
-                        const float p0 = ex2_approx(fmaf(__uint_as_float(s[c]), sl2, -mb));
-                        const float p1 = ex2_approx(fmaf(__uint_as_float(s[c + 1]), sl2, -mb));
+                        float p0, p1;
+                        fma2(p0, p1, __uint_as_float(s[c]), __uint_as_float(s[c + 1]), sl2, sl2, -mb, -mb);
+                        p0 = ex2_approx(p0);
+                        p1 = ex2_approx(p1);
                         const int x = (c >> 1) & 1;
-                        sp[2 * x] += p0;
-                        sp[2 * x + 1] += p1;
+                        add2(sp[2 * x], sp[2 * x + 1], p0, p1);
                         s[c >> 1] = Op::pack(p0, p1);
                     }
-                    if (CF::kOwnP && kt > walk.k0) {
+                    if (CF::kOwnP && kt > k0) {
                         // the P V before this one has read P, and left O
                         ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o(u), outs & 1u, wc));
                         if (!ok) break;
@@ -668,7 +678,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                     tmem_st32(tP, *reinterpret_cast<const uint32_t(*)[32]>(&s[0]));
                     tmem_st32(tP + 32u, *reinterpret_cast<const uint32_t(*)[32]>(&s[32]));
                     l = l * alpha + ((sp[0] + sp[1]) + (sp[2] + sp[3]));
-                    if (kt > walk.k0 && __any_sync(0xffffffffu, raise)) {
+                    if (kt > k0 && __any_sync(0xffffffffu, raise)) {
                         // O_u is idle: without its own P, the S_u just read was issued
                         // after the last P_u V and its end covers every earlier MMA.
 #pragma unroll
@@ -682,7 +692,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         }
                     }
                     tmem_st_wait();
-                    if (kt >= walk.first_masked()) {
+                    if (kt >= masked) {
                         // warps 2-3 have looked through V (see there)
                         const int vs = n % CF::kStages;
                         ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_check(vs), looked >> vs & 1u, wc));
@@ -693,16 +703,16 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         const bool upper = *(volatile int*)&s_odd[vs][1] == mark;
                         if (lower || upper) {
                             add_seen_keys<D, kHalf>(a, a.table + (long long)walk.req * a.table_stride, walk.kvh, key0,
-                                                    min(kBN, keys - key0), lim, lower, upper, tP, tO, kt == walk.k0);
-                            if (kt == walk.k0) *(volatile int*)&s_seen[u] = (int)(piece + 1);
+                                                    min(kBN, walk.w.keys(walk.t) - key0), lim, lower, upper, tP, tO, kt == k0);
+                            if (kt == k0) *(volatile int*)&s_seen[u] = (int)(piece + 1);
                         }
                     }
                     tc_fence_before();
                     mbar_arrive(bar_p_full(u));
                 }
             } else {
-                n += (uint32_t)(walk.first_masked() - walk.k0);
-                for (int kt = walk.first_masked(); kt < k1; ++kt, ++n) looked ^= 1u << (n % CF::kStages);
+                n += (uint32_t)(masked - k0);
+                for (int kt = masked; kt < k1; ++kt, ++n) looked ^= 1u << (n % CF::kStages);
             }
             if (ok && u < nu) ok = __all_sync(0xffffffffu, mbar_wait_inline(bar_o(u), outs++ & 1u, wc));
             if (ok && u < nu) {
@@ -754,7 +764,11 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                 }
             }
             ++piece;
-        } while (ok && walk.next());
+            __syncwarp();
+            if (lane == 0) more = place->next();
+            more = __shfl_sync(0xffffffffu, more, 0);
+            __syncwarp();
+        }
     }
 
     tc_fence_before();
