@@ -131,34 +131,33 @@ cudaError_t launch_after(bool follows, void (*kernel)(Params...), dim3 grid, int
 // request is served by paged_rows_kernel, above by paged_tiles_kernel.
 constexpr int kFewRows = 16;
 
-template <int D, bool kHalf>
-cudaError_t launch_rows(const ra::paged::AttnParams& p, const ra::paged::Workspace& ws, ra::paged::RowRange range,
-                        int blocks, cudaStream_t s)
-{
-    namespace pr = ra::paged::rows;
-    ra::prof::Scope ps(ra::prof::kPagedRows, s);
-    const cudaError_t r = launch_after(false, pr::paged_rows_kernel<D, kHalf>, dim3(blocks), pr::kThreads,
-                                       pr::Cfg<D>::kSmemBytes, s, p, ws, range);
-    ps.done();
-    return r;
-}
-
-// The tensor maps of paged_tiles_kernel.
+// The tensor maps of both kernels; paged_tiles_kernel alone reads Q by one.
 struct TileMaps {
     CUtensorMap q, k, v;
 };
 
-int make_tile_maps(TileMaps* m, const ra::paged::AttnParams& p, bool half, int d, int tok_tile, int box_rows)
+int make_maps(TileMaps* m, const ra::paged::AttnParams& p, bool half, int d, int tok_tile, int box_rows, bool with_q)
 {
-    int rc = make_paged_map(&m->q, p.q, half, d, {p.group, p.tokens, p.kv_heads},
-                            {p.q_head, p.q_tok, p.q_head * p.group}, {p.group, tok_tile, 1});
-    if (rc == RA_OK)
-        rc = make_paged_map(&m->k, p.kc, half, d, {p.page_size, p.kv_heads, p.num_pages}, {p.lk.st, p.lk.sh, p.lk.sp},
+    int rc = make_paged_map(&m->k, p.kc, half, d, {p.page_size, p.kv_heads, p.num_pages}, {p.lk.st, p.lk.sh, p.lk.sp},
                             {box_rows, 1, 1});
     if (rc == RA_OK)
         rc = make_paged_map(&m->v, p.vc, half, d, {p.page_size, p.kv_heads, p.num_pages}, {p.lv.st, p.lv.sh, p.lv.sp},
                             {box_rows, 1, 1});
+    if (rc == RA_OK && with_q)
+        rc = make_paged_map(&m->q, p.q, half, d, {p.group, p.tokens, p.kv_heads},
+                            {p.q_head, p.q_tok, p.q_head * p.group}, {p.group, tok_tile, 1});
     return rc;
+}
+
+template <int D, bool kHalf>
+cudaError_t launch_rows(const TileMaps& maps, const ra::paged::rows::RowsParams& p, int blocks, cudaStream_t s)
+{
+    namespace pr = ra::paged::rows;
+    ra::prof::Scope ps(ra::prof::kPagedRows, s);
+    const cudaError_t r = launch_after(false, pr::paged_rows_kernel<D, kHalf>, dim3(blocks), pr::kThreads,
+                                       pr::Cfg<D>::kSmemBytes, s, maps.k, maps.v, p);
+    ps.done();
+    return r;
 }
 
 template <int D, bool kHalf>
@@ -186,15 +185,15 @@ int launch_attn(const ra::paged::AttnParams& p, void* workspace, int max_q, int 
     bool run_rows = true, run_tiles = true;
     if ((long long)max_q * p.group <= kFewRows || (long long)p.tokens * p.group <= kFewRows) run_tiles = false;
     else if (p.group > kFewRows || (long long)p.n * max_q <= p.tokens) run_rows = false;
+    const int box_rows = std::min(p.page_size & -p.page_size, tiles::kBN);
     TileMaps maps;
-    tiles::TileParams tp{p, big, {run_rows ? kFewRows : 0, INT_MAX}, tiles::kBM / p.group,
-                         std::min(p.page_size & -p.page_size, tiles::kBN), g_wait_limit_ns.load()};
-    if (run_tiles) {
-        const int rc = make_tile_maps(&maps, p, kHalf, D, tp.tok_tile, tp.box_rows);
-        if (rc != RA_OK) return rc;
-    }
+    const int rc = make_maps(&maps, p, kHalf, D, tiles::kBM / p.group, box_rows, run_tiles);
+    if (rc != RA_OK) return rc;
+    const rows::RowsParams rp{p, few, {0, run_tiles ? kFewRows : INT_MAX}, box_rows, g_wait_limit_ns.load()};
+    const tiles::TileParams tp{p, big, {run_rows ? kFewRows : 0, INT_MAX}, tiles::kBM / p.group, box_rows,
+                               g_wait_limit_ns.load()};
     cudaError_t e = cudaSuccess;
-    if (run_rows) e = launch_rows<D, kHalf>(p, few, {0, run_tiles ? kFewRows : INT_MAX}, blocks, s);
+    if (run_rows) e = launch_rows<D, kHalf>(maps, rp, blocks, s);
     if (run_tiles && e == cudaSuccess) e = launch_tiles<D, kHalf>(run_rows, maps, tp, blocks, s);
     if (e == cudaSuccess) {
         const int first = run_tiles ? 0 : kBigSlices, last = run_rows ? kBigSlices + 1 : kBigSlices;

@@ -96,15 +96,6 @@ __device__ __forceinline__ float max_nan(float a, float b)
     return r;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool take)
-{
-    const uint32_t bytes = take ? 16u : 0u;   // 0: the 16 bytes are filled with zeros, src is not read
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr)
 {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

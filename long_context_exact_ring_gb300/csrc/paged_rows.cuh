@@ -11,17 +11,22 @@ namespace rows {
 constexpr int kRows = kRowsTile;        // packed rows of a tile: one m16n8k16 operand
 constexpr int kKeys = 16;               // keys of a warp's step
 constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kThreads = 384;
+// Warp 0 copies, warps 4-11 compute; 1-3 lend them their registers: 128 * 72 +
+// 256 * 216 are the 384 * 168 that the block starts with.
+constexpr int kFewRegs = 72, kManyRegs = 216;
 constexpr int kUnit = kKeys * kWarps;   // keys of a block's step, and of the smallest piece of work
 
 template <int D>
 struct Cfg {
-    static constexpr int kChunkBytes = kKeys * D * 2;              // a warp's K (or V) of one step
+    static constexpr int kBoxes = D / 64;                          // 64-column boxes of a row
+    static constexpr int kBoxBytes = 64 * kUnit * 2;
+    static constexpr int kTileBytes = kUnit * D * 2;               // K (or V) of a unit
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kWarpBytes = 2 * kChunkBytes * kStages;
     static constexpr int kStateBytes = kRows * D * 4 + 2 * kRows * 4;
-    static constexpr int kOffMerge = kWarps * kWarpBytes;
-    static constexpr int kSmemBytes = kOffMerge + kWarps / 2 * kStateBytes;
+    static constexpr int kOffMerge = 2 * kStages * kTileBytes;
+    static constexpr int kOffBar = kOffMerge + kWarps / 2 * kStateBytes;
+    static constexpr int kSmemBytes = kOffBar + 256 + 1024;        // + alignment slack
 };
 
 // What a tile costs beside its keys, in units: the states of eight warps are
@@ -96,138 +101,170 @@ struct Walk {
     }
 };
 
+struct RowsParams {
+    AttnParams a;
+    Workspace ws;
+    RowRange range;
+    int box_rows;            // rows of a K/V box: the largest power of two in page_size, at most 128
+    uint64_t wait_limit_ns;
+};
+
 // The work is the list of (request, key/value head, tile of 16 packed rows,
 // 128 keys); every block takes an equal, contiguous share of it, so a single
-// long context keeps all SMs reading as well as many short ones do.  Every
-// warp streams its own 16 keys out of each 128 through its own ring of
-// stages (asynchronous copies, no barrier between warps) and keeps its own
-// softmax state; the states of the eight warps are merged in pairs at the end
-// of a tile, or of the block's part of it, and parts by paged_join_kernel.  A
-// warp's copies run ahead of its products into the block's next tile, so the
-// SM goes on reading while states are merged and results are written.
+// long context keeps all SMs reading as well as many short ones do.  One warp
+// copies K and V, page by page (TMA), as far ahead as there are stages, into
+// the block's next tiles too; eight warps take 16 of each 128 keys and keep a
+// softmax state each.  The states are merged in pairs at the end of a tile, or
+// of the block's part of it, and parts by paged_join_kernel.
 //
-// Bound by HBM: K and V are read once per 16 packed rows.
+// Bound by HBM: K and V are read once per 16 packed rows.  (mma.sync: 16 rows
+// leave the tcgen05 tile of 128 empty, and the products are not the bound.)
+// ROWS_FIGURES
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParams p, const Workspace ws, const RowRange range)
+__global__ void __launch_bounds__(kThreads, 1)
+paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                  const __grid_constant__ RowsParams rp)
 {
     using C = Cfg<D>;
     using Op = Operand<kHalf>;
-    extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ long long s_scratch[kWarps];
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ long long s_scratch[kThreads / 32];
     __shared__ long long s_offset;
-    __shared__ int s_req;
+    __shared__ int s_req, s_abort;
+    const AttnParams& p = rp.a;
+    const uint32_t raw_base = smem_u32(smem_raw);
+    const uint32_t base = (raw_base + 1023u) & ~1023u;
+    uint8_t* gbase = smem_raw + (base - raw_base);
+    const uint32_t bar0 = base + C::kOffBar;
+    auto bar_full = [&](int s) { return bar0 + 8u * s; };                          // copies -> products
+    auto bar_empty = [&](int s) { return bar0 + 8u * (C::kStages + s); };          // products -> copies
+    auto bar_state = [&](int w) { return bar0 + 8u * (2 * C::kStages + w); };      // warp w's state written
+    auto bar_read = [&](int w) { return bar0 + 8u * (2 * C::kStages + 8 + w); };   // buffer w's last state read
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, t4 = lane & 3;
-    const uint32_t s_my = smem_u32(smem_raw) + warp * C::kWarpBytes;
     let_next_start();
 
     // ---- this block's share of the work
     const int per = (p.n + kThreads - 1) / kThreads;
     const int i0 = min(p.n, tid * per), i1 = min(p.n, i0 + per);
     long long mine = 0, total;
-    for (int i = i0; i < i1; ++i) mine += Walk::cost(p, range, i);
+    for (int i = i0; i < i1; ++i) mine += Walk::cost(p, rp.range, i);
     const long long before = block_exclusive_sum(mine, s_scratch, &total);
     const int b = blockIdx.x;
     const Share share = share_of(total, gridDim.x, b);
-    if (tid < 2) ws.info[2 * b + tid].req = -1;
+    if (tid < 2) rp.ws.info[2 * b + tid].req = -1;
     if (share.count == 0) return;
     if (before <= share.start && share.start < before + mine) {
         long long x = share.start - before;
         int i = i0;
-        for (long long c; x >= (c = Walk::cost(p, range, i)); ++i) x -= c;
+        for (long long c; x >= (c = Walk::cost(p, rp.range, i)); ++i) x -= c;
         s_req = i;
         s_offset = x;
     }
-    __syncthreads();
-    Walk walk(p, range, s_req, s_offset, share.count);
-    if (walk.empty()) return;
-
-    // ---- copies, ahead of the products.  Page sizes are multiples of 8, so 8
-    // keys share a page.  A lane holds the page of one half of one of 16 steps,
-    // and another for the 16 behind those, so no copy waits for its page.
-    constexpr int kPieces = D / 8;                   // 16-byte pieces of a row
-    constexpr int kRowsPerOp = 32 / kPieces;
-    Walk ahead = walk;
-    int a_key, a_keys, a_kvh, a_step, a_stage = 0, page_now, page_then;
-    bool a_more = true;
-    const int* a_table;
-    auto fetch_page = [&](int key) {
-        key += (lane >> 1) * kUnit + (lane & 1) * 8;
-        return key < a_keys ? __ldg(a_table + page_index(key, p.page_size, p.page_shift)) : 0;
-    };
-    auto enter = [&]() {
-        a_key = ahead.u0 * kUnit + warp * kKeys;
-        a_keys = ahead.keys();
-        a_kvh = ahead.kvh();
-        a_table = p.table + (long long)ahead.req * p.table_stride;
-        a_step = 0;
-        page_now = fetch_page(a_key);
-        page_then = fetch_page(a_key + 16 * kUnit);
-    };
-    auto copy_next = [&]() {
-        while (a_more && a_key >= a_keys) {
-            a_more = ahead.next();
-            if (a_more) enter();
+    if (tid == 0) {
+        s_abort = 0;
+        for (int s = 0; s < C::kStages; ++s) {
+            mbar_init(bar_full(s), 1);
+            mbar_init(bar_empty(s), kWarps);
         }
-        if (a_more) {
-            long long kb[2], vb[2];
-            bool ok[2], bad = false;
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const int key = a_key + 8 * hf, page = __shfl_sync(0xffffffffu, page_now, 2 * a_step + hf);
-                ok[hf] = key < a_keys;
-                if (!page_ok(page, p.num_pages)) {
-                    ok[hf] = false;
-                    bad = true;
+        for (int w = 0; w < kWarps; ++w) mbar_init(bar_state(w), 1);
+        for (int w = 0; w < kWarps / 2; ++w) mbar_init(bar_read(w), 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    Walk walk(p, rp.range, s_req, s_offset, share.count);
+    if (walk.empty()) return;
+    const WaitCtl wc{&s_abort, p.status, rp.wait_limit_ns};
+    auto wait_all = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_inline(bar, parity & 1u, wc));
+    };
+
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        if (warp > 0) return;
+        // ------------------------------------------------------------ copies
+        const int boxes = kUnit / rp.box_rows * C::kBoxes;      // at most 32: one for each lane
+        const int box = lane / C::kBoxes, half = lane % C::kBoxes;
+        const uint32_t box_dst = (uint32_t)(half * C::kBoxBytes + box * rp.box_rows * 128);
+        if (lane == 0) {
+            tma_prefetch_desc(&map_k);
+            tma_prefetch_desc(&map_v);
+        }
+        bool ok = true;
+        uint32_t n = 0;
+        do {
+            const int* table = p.table + (long long)walk.req * p.table_stride;
+            const int keys = walk.keys(), kvh = walk.kvh(), u1 = walk.u1;
+            auto page_at = [&](int u) {
+                const int key = u * kUnit + box * rp.box_rows;
+                return lane < boxes && u < u1 && key < keys ? table[page_index(key, p.page_size, p.page_shift)] : 0;
+            };
+            int page = page_at(walk.u0), then = page_at(walk.u0 + 1);
+            for (int u = walk.u0; u < u1; ++u, ++n) {
+                const int s = n % C::kStages;
+                const int key = u * kUnit + box * rp.box_rows;
+                const bool load = lane < boxes && key < keys;
+                // a page outside the pool: a coordinate outside the map, which reads as zeros
+                int coord = page;
+                if (load && !page_ok(page, p.num_pages)) {
+                    coord = p.num_pages;
+                    atomicOr(p.status, kStatusBadPage);
                 }
                 const int off = key - page_index(key, p.page_size, p.page_shift) * p.page_size;
-                kb[hf] = ok[hf] ? row_offset(p.lk, page, off, a_kvh) : 0;
-                vb[hf] = ok[hf] ? row_offset(p.lv, page, off, a_kvh) : 0;
+                page = then;
+                then = page_at(u + 2);
+                const uint32_t bytes = 2u * (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * rp.box_rows * 128u;
+                if (!(ok = wait_all(bar_empty(s), (n / C::kStages) + 1u))) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar_full(s), bytes);
+                __syncwarp();
+                if (load) {
+                    const uint32_t dst = base + 2 * s * C::kTileBytes + box_dst;
+                    tma_load_4d(dst, &map_k, bar_full(s), 64 * half, off, kvh, coord);
+                    tma_load_4d(dst + C::kTileBytes, &map_v, bar_full(s), 64 * half, off, kvh, coord);
+                }
             }
-            if (bad && lane == 0) atomicOr(p.status, kStatusBadPage);
-            const uint32_t sK = s_my + a_stage * 2 * C::kChunkBytes, sV = sK + C::kChunkBytes;
-#pragma unroll
-            for (int x = 0; x < kKeys / kRowsPerOp; ++x) {
-                const int row = x * kRowsPerOp + lane / kPieces, piece = lane % kPieces;
-                const int hf = row >> 3, in = row & 7;
-                const bool take = ok[hf] && a_key + row < ahead.r.len;
-                const uint32_t dst = (uint32_t)(row * D * 2 + ((piece ^ in) << 4));
-                cp_async16(sK + dst, p.kc + kb[hf] + (take ? in * p.lk.st : 0) + piece * 8, take);
-                cp_async16(sV + dst, p.vc + vb[hf] + (take ? in * p.lv.st : 0) + piece * 8, take);
-            }
-            a_stage = a_stage + 1 == C::kStages ? 0 : a_stage + 1;
-            a_key += kUnit;
-            if (++a_step == 16) {
-                a_step = 0;
-                page_now = page_then;
-                page_then = fetch_page(a_key + 16 * kUnit);
-            }
-        }
-        cp_async_commit();
-    };
-    enter();
-#pragma unroll 1
-    for (int x = 0; x < C::kStages - 1; ++x) copy_next();
+        } while (ok && walk.next());
+        // Every copy lands before the block's shared memory goes.
+        volatile int dummy = 0;
+        const WaitCtl drain{&dummy, p.status, 200000000ull};
+        for (uint32_t x = n > C::kStages ? n - C::kStages : 0; x < n; ++x)
+            mbar_wait_inline(bar_full(x % C::kStages), (x / C::kStages) & 1u, drain);
+        return;
+    }
 
-    int stage = 0;
-    do {
+    // -------------------------------------------------------------- products
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+    const int w = warp - 4, g = lane >> 2, t4 = lane & 3;
+    // the tile's rows 16 w .. 16 w + 15 in a stage; 16-byte pieces swizzled by row
+    const int k_row = (lane & 7) + ((lane >> 4) << 3), v_row = lane & 15;
+    const uint32_t k_base = base + (uint32_t)(16 * w + k_row) * 128u;
+    const uint32_t v_base = base + C::kTileBytes + (uint32_t)(16 * w + v_row) * 128u;
+    auto load_q = [&](uint32_t (&qa)[D / 16][4]) {
         const int row0 = walk.row0(), rows = walk.rows(), kvh = walk.kvh();
-        const Request r = walk.r;
-        const int keys = walk.keys();
-        // the two rows of this thread: last key each attends to
-        int lim[2];
-        uint32_t qa[D / 16][4];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = row0 + min(g + 8 * e, rows - 1);
             const int tok = row / p.group, head = kvh * p.group + (row - tok * p.group);
-            lim[e] = p.causal ? min(r.len, r.len - r.q + tok + 1) - 1 : r.len - 1;
-            const uint16_t* q = p.q + (long long)(r.first + tok) * p.q_tok + (long long)head * p.q_head + t4 * 2;
+            const uint16_t* q = p.q + (long long)(walk.r.first + tok) * p.q_tok + (long long)head * p.q_head + t4 * 2;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 qa[k][e] = *reinterpret_cast<const uint32_t*>(q + k * 16);
                 qa[k][2 + e] = *reinterpret_cast<const uint32_t*>(q + k * 16 + 8);
             }
+        }
+    };
+    uint32_t qa[D / 16][4];
+    load_q(qa);
+    uint32_t n = 0, piece = 0;
+    bool ok = true, more = true;
+    while (ok && more) {
+        const int row0 = walk.row0(), rows = walk.rows(), kvh = walk.kvh(), keys = walk.keys();
+        const Request r = walk.r;
+        // the two rows of this thread: last key each attends to
+        int lim[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int tok = (row0 + min(g + 8 * e, rows - 1)) / p.group;
+            lim[e] = p.causal ? min(r.len, r.len - r.q + tok + 1) - 1 : r.len - 1;
         }
         // smallest limit of the tile
         const int lim_first = p.causal ? r.len - r.q + row0 / p.group : r.len - 1;
@@ -242,28 +279,33 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
 #pragma unroll
             for (int y = 0; y < 4; ++y) st.acc[x][y] = 0.f;
 
-        for (int key0 = walk.u0 * kUnit + warp * kKeys; key0 < keys; key0 += kUnit) {
-            copy_next();
-            cp_async_wait<C::kStages - 1>();
-            __syncwarp();
-            const uint32_t sK = s_my + stage * 2 * C::kChunkBytes, sV = sK + C::kChunkBytes;
-            stage = stage + 1 == C::kStages ? 0 : stage + 1;
+        for (int u = walk.u0; u < walk.u1; ++u, ++n) {
+            const int stage = n % C::kStages, key0 = u * kUnit + w * kKeys;
+            if (!(ok = wait_all(bar_full(stage), n / C::kStages))) break;
+            if (key0 >= keys) {
+                if (lane == 0) mbar_arrive(bar_empty(stage));
+                continue;
+            }
+            const uint32_t sK = k_base + 2 * stage * C::kTileBytes, sV = v_base + 2 * stage * C::kTileBytes;
 
-            // ---- S = Q K^T: 16 rows x 16 keys
-            float s[2][4];
+            // ---- S = Q K^T: 16 rows x 16 keys, even and odd k-steps apart
+            float s[2][4], s2[2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int y = 0; y < 4; ++y) s[x][y] = 0.f;
+                for (int y = 0; y < 4; ++y) s[x][y] = s2[x][y] = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
                 // matrices: keys 0-7 | 8-15, columns 16k..16k+7 | 16k+8..
-                const int row = (lane & 7) + ((lane >> 4) << 3), piece = 2 * k + ((lane >> 3) & 1);
-                uint32_t b[4];
-                ldmatrix4(b, sK + row * D * 2 + ((piece ^ (row & 7)) << 4));
-                Op::mma(s[0], qa[k], b[0], b[1]);
-                Op::mma(s[1], qa[k], b[2], b[3]);
+                uint32_t kb[4];
+                ldmatrix4(kb, sK + (k >> 2) * C::kBoxBytes + (((2 * (k & 3) + ((lane >> 3) & 1)) ^ (k_row & 7)) << 4));
+                Op::mma(k & 1 ? s2[0] : s[0], qa[k], kb[0], kb[1]);
+                Op::mma(k & 1 ? s2[1] : s[1], qa[k], kb[2], kb[3]);
             }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) s[x][y] += s2[x][y];
 
             // ---- softmax
             const bool masked = key0 + kKeys - 1 > lim_first;
@@ -310,60 +352,79 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
             pa[3] = Op::pack(s[1][2], s[1][3]);
 
             // ---- O += P V
-            bool odd = false;
-#pragma unroll
-            for (int x = 0; x < D / 16; ++x) {
+            auto load_v = [&](uint32_t (&vb)[4], int x) {
                 // matrices: keys 0-7 | 8-15 of columns 16x.., then of 16x + 8..
-                const int row = lane & 15, piece = 2 * x + (lane >> 4);
-                uint32_t b[4];
-                ldmatrix4_trans(b, sV + row * D * 2 + ((piece ^ (row & 7)) << 4));
-                if (!masked) {
-                    Op::mma(st.acc[2 * x], pa, b[0], b[1]);
-                    Op::mma(st.acc[2 * x + 1], pa, b[2], b[3]);
-                } else {
-                    odd |= Op::nonfinite(b[0]) || Op::nonfinite(b[1]) || Op::nonfinite(b[2]) || Op::nonfinite(b[3]);
+                ldmatrix4_trans(vb, sV + (x >> 2) * C::kBoxBytes + (((2 * (x & 3) + (lane >> 4)) ^ (v_row & 7)) << 4));
+            };
+            if (!masked) {
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    uint32_t vb[4];
+                    load_v(vb, x);
+                    Op::mma(st.acc[2 * x], pa, vb[0], vb[1]);
+                    Op::mma(st.acc[2 * x + 1], pa, vb[2], vb[3]);
                 }
-            }
-            if (masked) {
-                // A weight of 0 does not hide an infinity or a NaN in V, so
+            } else {
+                // Rows of V behind the last key in use hold anything: cleared.
+                // A weight of 0 does not hide an infinity or a NaN either, so
                 // where rows see different keys and V holds one, the keys are
                 // added one by one to the rows that see them.
-                if (!__any_sync(0xffffffffu, odd)) {
+                const int valid = keys - key0 - 2 * t4;      // of this thread's keys 2 t4 + {0, 1, 8, 9}
+                const uint32_t lo = (valid > 0 ? 0xffffu : 0u) | (valid > 1 ? 0xffff0000u : 0u);
+                const uint32_t hi = (valid > 8 ? 0xffffu : 0u) | (valid > 9 ? 0xffff0000u : 0u);
+                bool odd = false;
 #pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const int row = lane & 15, piece = 2 * x + (lane >> 4);
-                        uint32_t b[4];
-                        ldmatrix4_trans(b, sV + row * D * 2 + ((piece ^ (row & 7)) << 4));
-                        Op::mma(st.acc[2 * x], pa, b[0], b[1]);
-                        Op::mma(st.acc[2 * x + 1], pa, b[2], b[3]);
+                for (int x = 0; x < D / 16; ++x) {
+                    uint32_t vb[4];
+                    load_v(vb, x);
+                    odd |= Op::nonfinite(vb[0] & lo) || Op::nonfinite(vb[1] & hi) || Op::nonfinite(vb[2] & lo) ||
+                           Op::nonfinite(vb[3] & hi);
+                }
+                odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) {
+                    uint32_t vb[4];
+                    load_v(vb, x);
+                    vb[0] &= lo;
+                    vb[1] &= hi;
+                    vb[2] &= lo;
+                    vb[3] &= hi;
+                    if (!odd) {
+                        Op::mma(st.acc[2 * x], pa, vb[0], vb[1]);
+                        Op::mma(st.acc[2 * x + 1], pa, vb[2], vb[3]);
+                        continue;
                     }
-                } else {
-#pragma unroll
-                    for (int x = 0; x < D / 16; ++x) {
-                        const int row = lane & 15, piece = 2 * x + (lane >> 4);
-                        uint32_t b[4];
-                        ldmatrix4_trans(b, sV + row * D * 2 + ((piece ^ (row & 7)) << 4));
 #pragma unroll 1
-                        for (int key = 0; key < kKeys; ++key) {
-                            const uint32_t sel = ((key & 7) >> 1) == t4 ? (key & 1 ? 0xffff0000u : 0x0000ffffu) : 0u;
-                            const uint32_t lo = key < 8 ? sel : 0u, hi = key < 8 ? 0u : sel;
-                            const uint32_t a[4] = {pa[0] & lo, pa[1] & lo, pa[2] & hi, pa[3] & hi};
+                    for (int key = 0; key < kKeys; ++key) {
+                        const uint32_t sel = ((key & 7) >> 1) == t4 ? (key & 1 ? 0xffff0000u : 0x0000ffffu) : 0u;
+                        const uint32_t lower = key < 8 ? sel : 0u, upper = key < 8 ? 0u : sel;
+                        const uint32_t one[4] = {pa[0] & lower, pa[1] & lower, pa[2] & upper, pa[3] & upper};
 #pragma unroll
-                            for (int y = 0; y < 2; ++y) {
-                                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                                Op::mma(d, a, b[2 * y] & lo, b[2 * y + 1] & hi);
+                        for (int y = 0; y < 2; ++y) {
+                            float d[4] = {0.f, 0.f, 0.f, 0.f};
+                            Op::mma(d, one, vb[2 * y] & lower, vb[2 * y + 1] & upper);
 #pragma unroll
-                                for (int z = 0; z < 4; ++z)
-                                    if (key0 + key <= lim[z >> 1]) st.acc[2 * x + y][z] += d[z];
-                            }
+                            for (int z = 0; z < 4; ++z)
+                                if (key0 + key <= lim[z >> 1]) st.acc[2 * x + y][z] += d[z];
                         }
                     }
                 }
             }
             __syncwarp();     // the stage may be written again
+            if (lane == 0) mbar_arrive(bar_empty(stage));
         }
+        if (!ok) break;
 
-        // ---- merge the eight warps: 4-7 into 0-3, 2-3 into 0-1, 1 into 0
+        // the next piece's queries are on their way while this one is merged
+        const bool whole = walk.u0 == 0 && walk.u1 == walk.units;
+        const int slot = 2 * b + (walk.u0 == 0);
+        const PartInfo info{walk.req, kvh, row0, walk.u1 == walk.units};
+        more = walk.next();
+        if (more) load_q(qa);
+
+        // ---- merge the eight warps: 4-7 into 0-3, 2-3 into 0-1, 1 into 0.  Warp
+        // w writes buffer w & 3, which its reader has written or read before;
+        // warps 4-7 wait for the last reader of the piece before.
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 1);
@@ -371,11 +432,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
         }
 #pragma unroll 1
         for (int half = kWarps / 2; half > 0; half >>= 1) {
-            float* state = reinterpret_cast<float*>(smem_raw + C::kOffMerge + (warp & (half - 1)) * C::kStateBytes);
+            if (w >= 2 * half) continue;
+            const bool give = w >= half;
+            const int from = give ? w : w + half;       // the warp whose state is handed over
+            float* state = reinterpret_cast<float*>(gbase + C::kOffMerge + (from & 3) * C::kStateBytes);
             float4* acc = reinterpret_cast<float4*>(state) + lane;
             float* ml = state + kRows * D;
-            __syncthreads();          // the states are read
-            if (warp >= half && warp < 2 * half) {
+            if (give) {
+                if (half == kWarps / 2 && !(ok = wait_all(bar_read(w & 3), piece + 1u))) break;
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x)
                     acc[32 * x] = make_float4(st.acc[x][0], st.acc[x][1], st.acc[x][2], st.acc[x][3]);
@@ -386,9 +450,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
                         ml[kRows + g + 8 * e] = st.l[e];
                     }
                 }
-            }
-            __syncthreads();
-            if (warp < half) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar_state(w));
+            } else {
+                if (!(ok = wait_all(bar_state(from), piece))) break;
                 float mine[2], other[2];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -408,42 +473,45 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const AttnParam
                     st.acc[x][2] = st.acc[x][2] * mine[1] + v.z * other[1];
                     st.acc[x][3] = st.acc[x][3] * mine[1] + v.w * other[1];
                 }
+                // buffers 0 and 1 are last read by warp 0, as 4's and 1's
+                // state, 2 by warp 0 as 2's, 3 by warp 1 as 3's
+                __syncwarp();
+                if (lane == 0 && (from == 4 || from < 4)) mbar_arrive(bar_read(from & 3));
             }
         }
-        if (warp == 0) {
-            const bool whole = walk.u0 == 0 && walk.u1 == walk.units;
-            const int slot = 2 * b + (walk.u0 == 0);
+        if (!ok) break;
+        ++piece;
+        if (w != 0) continue;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = g + 8 * e;
-                if (whole) {
-                    if (row >= rows) continue;
-                    // no key, or none with a weight: O = 0, LSE = -inf
-                    const float inv = st.m[e] == -INFINITY ? 0.f : 1.f / st.l[e];
-                    const int tok = (row0 + row) / p.group, head = kvh * p.group + (row0 + row - tok * p.group);
-                    uint16_t* dst = p.o + (long long)(r.first + tok) * p.o_tok + (long long)head * p.o_head + 2 * t4;
+        for (int e = 0; e < 2; ++e) {
+            const int row = g + 8 * e;
+            if (whole) {
+                if (row >= rows) continue;
+                // no key, or none with a weight: O = 0, LSE = -inf
+                const float inv = st.m[e] == -INFINITY ? 0.f : 1.f / st.l[e];
+                const int tok = (row0 + row) / p.group, head = kvh * p.group + (row0 + row - tok * p.group);
+                uint16_t* dst = p.o + (long long)(r.first + tok) * p.o_tok + (long long)head * p.o_head + 2 * t4;
 #pragma unroll
-                    for (int x = 0; x < D / 8; ++x)
-                        *reinterpret_cast<uint32_t*>(dst + 8 * x) =
-                            Op::pack(st.acc[x][2 * e] * inv, st.acc[x][2 * e + 1] * inv);
-                    if (t4 == 0)
-                        p.lse[(long long)head * p.tokens + r.first + tok] =
-                            st.m[e] == -INFINITY ? -INFINITY
-                                                 : (st.m[e] - Op::kShift + log2f(st.l[e])) * 0.69314718055994531f;
-                } else {
+                for (int x = 0; x < D / 8; ++x)
+                    *reinterpret_cast<uint32_t*>(dst + 8 * x) =
+                        Op::pack(st.acc[x][2 * e] * inv, st.acc[x][2 * e + 1] * inv);
+                if (t4 == 0)
+                    p.lse[(long long)head * p.tokens + r.first + tok] =
+                        st.m[e] == -INFINITY ? -INFINITY
+                                             : (st.m[e] - Op::kShift + log2f(st.l[e])) * 0.69314718055994531f;
+            } else {
 #pragma unroll
-                    for (int x = 0; x < D / 8; ++x)
-                        reinterpret_cast<float2*>(part_columns(ws, slot, kRows, D, row, 8 * x + 2 * t4))[t4 & 1] =
-                            make_float2(st.acc[x][2 * e], st.acc[x][2 * e + 1]);
-                    if (t4 == 0) {
-                        ws.ml[slot * 2 * kRows + row] = st.m[e];
-                        ws.ml[slot * 2 * kRows + kRows + row] = st.l[e];
-                    }
+                for (int x = 0; x < D / 8; ++x)
+                    reinterpret_cast<float2*>(part_columns(rp.ws, slot, kRows, D, row, 8 * x + 2 * t4))[t4 & 1] =
+                        make_float2(st.acc[x][2 * e], st.acc[x][2 * e + 1]);
+                if (t4 == 0) {
+                    rp.ws.ml[slot * 2 * kRows + row] = st.m[e];
+                    rp.ws.ml[slot * 2 * kRows + kRows + row] = st.l[e];
                 }
             }
-            if (!whole && lane == 0) ws.info[slot] = PartInfo{walk.req, kvh, row0, walk.u1 == walk.units};
         }
-    } while (walk.next());
+        if (!whole && lane == 0) rp.ws.info[slot] = info;
+    }
 }
 
 }  // namespace rows
