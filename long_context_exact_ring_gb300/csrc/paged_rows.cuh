@@ -9,20 +9,23 @@ namespace paged {
 namespace rows {
 
 constexpr int kRows = kRowsTile;        // packed rows of a tile: one m16n8k16 operand
-constexpr int kKeys = 16;               // keys of a warp's step
-constexpr int kWarps = 8;
+constexpr int kWarps = 8;               // that compute
 constexpr int kThreads = 384;
 // Warp 0 copies, warps 4-11 compute; 1-3 lend them their registers: 128 * 72 +
 // 256 * 216 are the 384 * 168 that the block starts with.
 constexpr int kFewRegs = 72, kManyRegs = 216;
-constexpr int kUnit = kKeys * kWarps;   // keys of a block's step, and of the smallest piece of work
 
 template <int D>
 struct Cfg {
+    // Keys of a warp's step, and of the block's, the smallest piece of work: a
+    // step is a chain of waits, products and shuffles, so with half the bytes
+    // to a key it takes twice the keys.
+    static constexpr int kKeys = D == 128 ? 16 : 32;
+    static constexpr int kUnit = kKeys * kWarps;
     static constexpr int kBoxes = D / 64;                          // 64-column boxes of a row
     static constexpr int kBoxBytes = 64 * kUnit * 2;
     static constexpr int kTileBytes = kUnit * D * 2;               // K (or V) of a unit
-    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kStages = 3;
     static constexpr int kStateBytes = kRows * D * 4 + 2 * kRows * 4;
     static constexpr int kOffMerge = 2 * kStages * kTileBytes;
     static constexpr int kOffBar = kOffMerge + kWarps / 2 * kStateBytes;
@@ -34,7 +37,8 @@ struct Cfg {
 // ragged contexts up to 16K: 365 us without it, 355 with 1, 340 with 2, 343 with 3.
 constexpr int kExtra = 2;
 
-// A block's place in its share: units [u0, u1) of 128 keys of a tile.
+// A block's place in its share: units [u0, u1) of kUnit keys of a tile.
+template <int kUnit>
 struct Walk {
     const AttnParams& p;
     const RowRange& range;
@@ -110,10 +114,10 @@ struct RowsParams {
 };
 
 // The work is the list of (request, key/value head, tile of 16 packed rows,
-// 128 keys); every block takes an equal, contiguous share of it, so a single
+// kUnit keys); every block takes an equal, contiguous share of it, so a single
 // long context keeps all SMs reading as well as many short ones do.  One warp
 // copies K and V, page by page (TMA), as far ahead as there are stages, into
-// the block's next tiles too; eight warps take 16 of each 128 keys and keep a
+// the block's next tiles too; eight warps take an eighth of a unit's keys and keep a
 // softmax state each.  The states are merged in pairs at the end of a tile, or
 // of the block's part of it, and parts by paged_join_kernel.
 //
@@ -127,6 +131,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 {
     using C = Cfg<D>;
     using Op = Operand<kHalf>;
+    using Walk = rows::Walk<C::kUnit>;
+    constexpr int kKeys = C::kKeys, kUnit = C::kUnit, kTiles8 = kKeys / 8, kSteps16 = kKeys / 16;
     extern __shared__ uint8_t smem_raw[];
     __shared__ long long s_scratch[kThreads / 32];
     __shared__ long long s_offset;
@@ -234,10 +240,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     // -------------------------------------------------------------- products
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
     const int w = warp - 4, g = lane >> 2, t4 = lane & 3;
-    // the tile's rows 16 w .. 16 w + 15 in a stage; 16-byte pieces swizzled by row
+    // the warp's rows of a stage, kKeys w and on; 16-byte pieces swizzled by row
     const int k_row = (lane & 7) + ((lane >> 4) << 3), v_row = lane & 15;
-    const uint32_t k_base = base + (uint32_t)(16 * w + k_row) * 128u;
-    const uint32_t v_base = base + C::kTileBytes + (uint32_t)(16 * w + v_row) * 128u;
+    const uint32_t k_base = base + (uint32_t)(kKeys * w + k_row) * 128u;
+    const uint32_t v_base = base + C::kTileBytes + (uint32_t)(kKeys * w + v_row) * 128u;
     auto load_q = [&](uint32_t (&qa)[D / 16][4]) {
         const int row0 = walk.row0(), rows = walk.rows(), kvh = walk.kvh();
 #pragma unroll
@@ -288,29 +294,33 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
             const uint32_t sK = k_base + 2 * stage * C::kTileBytes, sV = v_base + 2 * stage * C::kTileBytes;
 
-            // ---- S = Q K^T: 16 rows x 16 keys, even and odd k-steps apart
-            float s[2][4], s2[2][4];
+            // ---- S = Q K^T: 16 rows x kKeys keys, even and odd k-steps apart
+            float s[kTiles8][4], s2[kTiles8][4];
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < kTiles8; ++x)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) s[x][y] = s2[x][y] = 0.f;
 #pragma unroll
             for (int k = 0; k < D / 16; ++k) {
-                // matrices: keys 0-7 | 8-15, columns 16k..16k+7 | 16k+8..
-                uint32_t kb[4];
-                ldmatrix4(kb, sK + (k >> 2) * C::kBoxBytes + (((2 * (k & 3) + ((lane >> 3) & 1)) ^ (k_row & 7)) << 4));
-                Op::mma(k & 1 ? s2[0] : s[0], qa[k], kb[0], kb[1]);
-                Op::mma(k & 1 ? s2[1] : s[1], qa[k], kb[2], kb[3]);
+#pragma unroll
+                for (int z = 0; z < kSteps16; ++z) {
+                    // matrices: keys 0-7 | 8-15, columns 16k..16k+7 | 16k+8..
+                    uint32_t kb[4];
+                    ldmatrix4(kb, sK + z * 2048 + (k >> 2) * C::kBoxBytes +
+                                      (((2 * (k & 3) + ((lane >> 3) & 1)) ^ (k_row & 7)) << 4));
+                    Op::mma(k & 1 ? s2[2 * z] : s[2 * z], qa[k], kb[0], kb[1]);
+                    Op::mma(k & 1 ? s2[2 * z + 1] : s[2 * z + 1], qa[k], kb[2], kb[3]);
+                }
             }
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < kTiles8; ++x)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) s[x][y] += s2[x][y];
 
             // ---- softmax
             const bool masked = key0 + kKeys - 1 > lim_first;
 #pragma unroll
-            for (int x = 0; x < 2; ++x)
+            for (int x = 0; x < kTiles8; ++x)
 #pragma unroll
                 for (int y = 0; y < 4; ++y) {
                     s[x][y] *= p.scale_log2;
@@ -319,7 +329,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float mx = max_nan(max_nan(s[0][2 * e], s[0][2 * e + 1]), max_nan(s[1][2 * e], s[1][2 * e + 1]));
+                float mx = max_nan(s[0][2 * e], s[0][2 * e + 1]);
+#pragma unroll
+                for (int x = 1; x < kTiles8; ++x) mx = max_nan(mx, max_nan(s[x][2 * e], s[x][2 * e + 1]));
                 mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = max_nan(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float m = max_nan(st.m[e], mx);
@@ -328,7 +340,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                 const float ref = m == -INFINITY ? 0.f : m - Op::kShift;
                 float sum = 0.f;
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < kTiles8; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         const float w = ex2_approx(s[x][2 * e + y] - ref);
@@ -345,67 +357,78 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             }
             // Weights rounded to the operand type (half a step of 2^-9 or
             // 2^-12 each); l sums them unrounded.
-            uint32_t pa[4];
-            pa[0] = Op::pack(s[0][0], s[0][1]);
-            pa[1] = Op::pack(s[0][2], s[0][3]);
-            pa[2] = Op::pack(s[1][0], s[1][1]);
-            pa[3] = Op::pack(s[1][2], s[1][3]);
+            uint32_t pa[kSteps16][4];
+#pragma unroll
+            for (int z = 0; z < kSteps16; ++z) {
+                pa[z][0] = Op::pack(s[2 * z][0], s[2 * z][1]);
+                pa[z][1] = Op::pack(s[2 * z][2], s[2 * z][3]);
+                pa[z][2] = Op::pack(s[2 * z + 1][0], s[2 * z + 1][1]);
+                pa[z][3] = Op::pack(s[2 * z + 1][2], s[2 * z + 1][3]);
+            }
 
             // ---- O += P V
-            auto load_v = [&](uint32_t (&vb)[4], int x) {
+            auto load_v = [&](uint32_t (&vb)[4], int z, int x) {
                 // matrices: keys 0-7 | 8-15 of columns 16x.., then of 16x + 8..
-                ldmatrix4_trans(vb, sV + (x >> 2) * C::kBoxBytes + (((2 * (x & 3) + (lane >> 4)) ^ (v_row & 7)) << 4));
+                ldmatrix4_trans(vb, sV + z * 2048 + (x >> 2) * C::kBoxBytes +
+                                        (((2 * (x & 3) + (lane >> 4)) ^ (v_row & 7)) << 4));
             };
             if (!masked) {
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    uint32_t vb[4];
-                    load_v(vb, x);
-                    Op::mma(st.acc[2 * x], pa, vb[0], vb[1]);
-                    Op::mma(st.acc[2 * x + 1], pa, vb[2], vb[3]);
-                }
+                for (int z = 0; z < kSteps16; ++z)
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        uint32_t vb[4];
+                        load_v(vb, z, x);
+                        Op::mma(st.acc[2 * x], pa[z], vb[0], vb[1]);
+                        Op::mma(st.acc[2 * x + 1], pa[z], vb[2], vb[3]);
+                    }
             } else {
                 // Rows of V behind the last key in use hold anything: cleared.
                 // A weight of 0 does not hide an infinity or a NaN either, so
                 // where rows see different keys and V holds one, the keys are
                 // added one by one to the rows that see them.
-                const int valid = keys - key0 - 2 * t4;      // of this thread's keys 2 t4 + {0, 1, 8, 9}
-                const uint32_t lo = (valid > 0 ? 0xffffu : 0u) | (valid > 1 ? 0xffff0000u : 0u);
-                const uint32_t hi = (valid > 8 ? 0xffffu : 0u) | (valid > 9 ? 0xffff0000u : 0u);
-                bool odd = false;
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    uint32_t vb[4];
-                    load_v(vb, x);
-                    odd |= Op::nonfinite(vb[0] & lo) || Op::nonfinite(vb[1] & hi) || Op::nonfinite(vb[2] & lo) ||
-                           Op::nonfinite(vb[3] & hi);
-                }
-                odd = __any_sync(0xffffffffu, odd);
+                for (int z = 0; z < kSteps16; ++z) {
+                    const int key16 = key0 + 16 * z;
+                    const int valid = keys - key16 - 2 * t4;     // of this thread's keys 2 t4 + {0, 1, 8, 9}
+                    const uint32_t lo = (valid > 0 ? 0xffffu : 0u) | (valid > 1 ? 0xffff0000u : 0u);
+                    const uint32_t hi = (valid > 8 ? 0xffffu : 0u) | (valid > 9 ? 0xffff0000u : 0u);
+                    bool odd = false;
 #pragma unroll
-                for (int x = 0; x < D / 16; ++x) {
-                    uint32_t vb[4];
-                    load_v(vb, x);
-                    vb[0] &= lo;
-                    vb[1] &= hi;
-                    vb[2] &= lo;
-                    vb[3] &= hi;
-                    if (!odd) {
-                        Op::mma(st.acc[2 * x], pa, vb[0], vb[1]);
-                        Op::mma(st.acc[2 * x + 1], pa, vb[2], vb[3]);
-                        continue;
+                    for (int x = 0; x < D / 16; ++x) {
+                        uint32_t vb[4];
+                        load_v(vb, z, x);
+                        odd |= Op::nonfinite(vb[0] & lo) || Op::nonfinite(vb[1] & hi) || Op::nonfinite(vb[2] & lo) ||
+                               Op::nonfinite(vb[3] & hi);
                     }
+                    odd = __any_sync(0xffffffffu, odd);
+#pragma unroll
+                    for (int x = 0; x < D / 16; ++x) {
+                        uint32_t vb[4];
+                        load_v(vb, z, x);
+                        vb[0] &= lo;
+                        vb[1] &= hi;
+                        vb[2] &= lo;
+                        vb[3] &= hi;
+                        if (!odd) {
+                            Op::mma(st.acc[2 * x], pa[z], vb[0], vb[1]);
+                            Op::mma(st.acc[2 * x + 1], pa[z], vb[2], vb[3]);
+                            continue;
+                        }
 #pragma unroll 1
-                    for (int key = 0; key < kKeys; ++key) {
-                        const uint32_t sel = ((key & 7) >> 1) == t4 ? (key & 1 ? 0xffff0000u : 0x0000ffffu) : 0u;
-                        const uint32_t lower = key < 8 ? sel : 0u, upper = key < 8 ? 0u : sel;
-                        const uint32_t one[4] = {pa[0] & lower, pa[1] & lower, pa[2] & upper, pa[3] & upper};
+                        for (int key = 0; key < 16; ++key) {
+                            const uint32_t sel = ((key & 7) >> 1) == t4 ? (key & 1 ? 0xffff0000u : 0x0000ffffu) : 0u;
+                            const uint32_t lower = key < 8 ? sel : 0u, upper = key < 8 ? 0u : sel;
+                            const uint32_t one[4] = {pa[z][0] & lower, pa[z][1] & lower, pa[z][2] & upper,
+                                                     pa[z][3] & upper};
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            float d[4] = {0.f, 0.f, 0.f, 0.f};
-                            Op::mma(d, one, vb[2 * y] & lower, vb[2 * y + 1] & upper);
+                            for (int y = 0; y < 2; ++y) {
+                                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                                Op::mma(d, one, vb[2 * y] & lower, vb[2 * y + 1] & upper);
 #pragma unroll
-                            for (int z = 0; z < 4; ++z)
-                                if (key0 + key <= lim[z >> 1]) st.acc[2 * x + y][z] += d[z];
+                                for (int e = 0; e < 4; ++e)
+                                    if (key16 + key <= lim[e >> 1]) st.acc[2 * x + y][e] += d[e];
+                            }
                         }
                     }
                 }
