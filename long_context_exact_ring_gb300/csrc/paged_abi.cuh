@@ -82,8 +82,10 @@ cudaError_t configure_paged_kernels()
     return e;
 }
 
-// 4-D tiled map of 2-byte elements with 128-byte swizzle, 64 columns wide.
-// Strides in elements; that of an extent-1 dimension is never stepped along
+// 4-D tiled map of 2-byte elements with 128-byte swizzle, 64 columns wide.  L2
+// fetches whole rows: with d 64, 256 bytes would bring the neighbouring head's
+// row too, which another block reads at another time (16 contexts of 8K, 16
+// heads: 128 us against 99).  Strides in elements; that of an extent-1 dimension is never stepped along
 // and is replaced by a valid one.
 int make_paged_map(CUtensorMap* map, const void* ptr, bool half, int d, const int (&extents)[3],
                    const long long (&strides)[3], const int (&box_rows)[3])
@@ -97,7 +99,8 @@ int make_paged_map(CUtensorMap* map, const void* ptr, bool half, int d, const in
     }
     const CUresult r = g_encode(map, half ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
                                 const_cast<void*>(ptr), dims, st, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_SWIZZLE_128B,
+                                d == 64 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         std::snprintf(g_last_error, sizeof(g_last_error), "cuTensorMapEncodeTiled (paged) failed (%d)", (int)r);
