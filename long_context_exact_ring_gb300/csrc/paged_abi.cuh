@@ -56,15 +56,31 @@ int page_shift(int page_size)
 
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
+// A kernel that moves registers between its warps waits for ever if it starts
+// with fewer than it hands out: refused here, before any launch.
+template <typename Kernel>
+cudaError_t check_registers(Kernel kernel, int threads, int few, int many)
+{
+    cudaFuncAttributes attr;
+    const cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    return attr.numRegs * threads >= 128 * few + (threads - 128) * many ? cudaSuccess : cudaErrorInvalidConfiguration;
+}
+
 template <int D, bool kHalf>
 cudaError_t configure_attn_kernels()
 {
-    cudaError_t e = cudaFuncSetAttribute(ra::paged::rows::paged_rows_kernel<D, kHalf>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         ra::paged::rows::Cfg<D>::kSmemBytes);
+    namespace pr = ra::paged::rows;
+    namespace pt = ra::paged::tiles;
+    cudaError_t e = check_registers(pr::paged_rows_kernel<D, kHalf>, pr::kThreads, pr::kFewRegs, pr::kManyRegs);
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(ra::paged::tiles::paged_tiles_kernel<D, kHalf>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, ra::paged::tiles::Cfg<D>::kSmemBytes);
+        e = check_registers(pt::paged_tiles_kernel<D, kHalf>, pt::kThreads, pt::kFewRegs, pt::kManyRegs);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(pr::paged_rows_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 pr::Cfg<D>::kSmemBytes);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(pt::paged_tiles_kernel<D, kHalf>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 pt::Cfg<D>::kSmemBytes);
     return e;
 }
 

@@ -52,6 +52,14 @@ int fail_cuda(cudaError_t e, const char* what)
 
 cudaError_t configure_paged_kernels();   // paged_abi.cuh
 
+// While it lives, this thread may make calls that a stream capture forbids
+// by default; none of the set-up's touches a stream.
+struct CaptureRelaxed {
+    cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+    CaptureRelaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+    ~CaptureRelaxed() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
 // Per-device set-up, once per device: resolve the status word's device
 // address, raise the kernels' shared-memory limits, find the TMA encoder.
 int device_state(DeviceState** out)
@@ -67,6 +75,8 @@ int device_state(DeviceState** out)
     }
     std::lock_guard<std::mutex> lock(g_mu);
     if (!st.ready) {
+        // the first call may come while a stream is being captured
+        CaptureRelaxed relaxed;
         if (!g_encode) {
             void* fn = nullptr;
             cudaDriverEntryPointQueryResult q;
@@ -80,9 +90,7 @@ int device_state(DeviceState** out)
         void* addr = nullptr;
         e = cudaGetSymbolAddress(&addr, g_status_word);
         if (e != cudaSuccess) return fail_cuda(e, "cudaGetSymbolAddress(status)");
-        st.status = static_cast<uint32_t*>(addr);
-        e = cudaMemset(st.status, 0, sizeof(uint32_t));
-        if (e != cudaSuccess) return fail_cuda(e, "cudaMemset(status)");
+        st.status = static_cast<uint32_t*>(addr);      // 0 when the library is loaded
         e = cudaDeviceGetAttribute(&st.num_sms, cudaDevAttrMultiProcessorCount, dev);
         if (e != cudaSuccess) return fail_cuda(e, "cudaDeviceGetAttribute");
         e = cudaFuncSetAttribute(ra::fwd::ring_fwd_kernel<64>,

@@ -333,6 +333,178 @@ def test_attn_other_stream_and_shared_workspace_of_two_graphs(ra):
     assert torch.equal(outs[1][0], other[0]) and torch.equal(outs[1][1], other[1])
 
 
+@pytest.mark.parametrize("H,H_kv", [(128, 1), (100, 1), (43, 1), (17, 1), (16, 1), (34, 2)])
+@pytest.mark.parametrize("news", [[1, 1, 0], [2, 3, 5]])
+def test_attn_large_groups(ra, H, H_kv, news):
+    """Groups that fill a tile of 128 rows, or leave some of it over."""
+    _check(ra, make([150, 64, 9], news, H, H_kv, 64, 8, torch.bfloat16, seed=H), True)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("news", [[1], [3, 1, 1], [40, 1, 9]])
+def test_attn_many_short_requests(ra, d, news):
+    """More requests than threads, each with a few keys; some without rows."""
+    rng = random.Random(d)
+    n = 700
+    lens = [rng.choice([0, 1, 7, 8, 33, 64, 100]) for _ in range(n)]
+    q = [min(rng.choice(news + [0]), max(a, 1)) for a in lens]
+    _check(ra, make(lens, q, 2, 1, d, 8, torch.bfloat16, seed=n), True)
+
+
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("d,page_size", [(64, 512), (128, 136)])
+def test_attn_one_context_over_all_blocks(ra, new, d, page_size):
+    """A context cut into as many parts as there are blocks, its last key
+    tiles short."""
+    for length in (152 * 128 + 1, 152 * 256 - 1):
+        x = make([length], [new], 2, 1, d, page_size, torch.float16, seed=new)
+        _check(ra, x, True)
+
+
+def test_attn_different_strides_for_keys_and_values(ra):
+    """K by tokens, V by heads, both inside wider storage; a wider table."""
+    x = make([90, 300], [1, 60], 8, 2, 64, 16, torch.bfloat16, seed=7)
+    num = x["k_cache"].shape[0]
+    k = torch.full((num, 16, 3, 72), float("nan"), dtype=torch.bfloat16)
+    v = torch.full((num + 2, 2, 24, 64), float("nan"), dtype=torch.bfloat16)
+    k[:, :, 1:, :64] = x["k_cache"]
+    v[:num, :, :16] = x["v_cache"].transpose(1, 2)
+    table = torch.full((2, x["table"].shape[1] + 5), 3, dtype=torch.int32)
+    table[:, :-5] = x["table"]
+    o, lse = ra.paged_attn_fwd(x["q"].cuda(), k.cuda()[:, :, 1:, :64], v.cuda()[:num, :, :16].transpose(1, 2),
+                               table.cuda()[:, :-5], x["seq_lens"].cuda(), x["cu_q"].cuda(), True)
+    o_ref, lse_ref, tol_o, tol_lse = attn_ref(x, True)
+    assert_close(o, o_ref, tol_o, "O")
+    assert_close(lse, lse_ref, tol_lse, "LSE")
+
+
+def test_attn_two_calls_at_once(ra):
+    """Two streams, each with a workspace of its own, over one pool."""
+    x = make([5000, 2000, 77], [1, 140, 30], 8, 2, 128, 16, torch.bfloat16, seed=12)
+    args = [x[n].cuda() for n in ("q", "k_cache", "v_cache", "table", "seq_lens", "cu_q")]
+    want = ra.paged_attn_fwd(*args, True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(10):
+        for s in streams:
+            got.append(ra.paged_attn_fwd(*args, True, stream=s))
+    torch.cuda.synchronize()
+    for o, lse in got:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+def test_attn_results_do_not_change_from_call_to_call(ra):
+    x = make([5000, 2000, 77] * 3, [1, 140, 30] * 3, 8, 2, 64, 16, torch.float16, seed=13)
+    want = _run(ra, x, True)
+    for _ in range(5):
+        got = _run(ra, x, True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_attn_part_contexts_merge_to_the_whole(ra):
+    """Attention over two halves of a context, merged as ring steps are."""
+    x = make([512], [1], 4, 2, 128, 16, torch.bfloat16, seed=15)
+    whole_o, whole_lse = _check(ra, x, False)
+    parts = []
+    for a in (0, 16):
+        y = dict(x, table=x["table"][:, a:a + 16].contiguous(), seq_lens=torch.tensor([256], dtype=torch.int32))
+        o, lse = _run(ra, y, False)
+        parts.append((o.float()[None].transpose(1, 2).contiguous(), lse[None].contiguous()))
+    (oa, la), (ob, lb) = parts
+    o, lse = ra.attn_merge_partials(oa, la, ob, lb)
+    # each part's O and the whole's are rounded: u max |O| each, the parts'
+    # weights summing to 1, and the weights' own rounding u max |v|
+    u = 2.0 ** -8
+    bound = 2 * u * max(float(x.abs().max()) for x in (oa, ob)) + 2 * u * 5
+    assert float((o[0].transpose(0, 1) - whole_o.float()).abs().max()) <= bound
+    assert float((lse[0] - whole_lse).abs().max()) <= 1e-4
+
+
+def test_attn_tiny_wait_limit_reports_or_completes(ra):
+    """Waits that run out end the kernels and are reported; the next call is
+    right again."""
+    x = make([4000, 900], [300, 1], 8, 2, 128, 16, torch.bfloat16, seed=16)
+    want = _run(ra, x, True)
+    assert ra.check_status() == ra.RA_OK
+    try:
+        ra.set_wait_limit_ns(1)
+        for _ in range(3):
+            _run(ra, x, True)
+            assert ra.check_status() in (ra.RA_OK, ra.RA_ERR_DEVICE_TIMEOUT)
+    finally:
+        ra.set_wait_limit_ns(0)
+    got = _run(ra, x, True)
+    assert ra.check_status() == ra.RA_OK
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+FIRST_CALL = """
+import torch
+import long_context_exact_ring_gb300 as ra
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+args = [i([0, 0]), i([3, 2]), i([[-1] * 4] * 2), i(list(range(8))), i([8, 0])]
+out = [torch.zeros(s, dtype=torch.int32, device="cuda") for s in (2, 3, 5, 2)]
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    ra.paged_kv_plan(*args, 8, 5, seq_lens_out=out[0], cu_q=out[1], slots=out[2], counts_out=out[3])
+g.replay()
+torch.cuda.synchronize()
+assert [x.tolist() for x in out] == [[3, 2], [0, 3, 5], [56, 57, 58, 48, 49], [6, 0]], out
+"""
+
+
+def test_first_call_inside_a_capture(ra):
+    """A process whose first call of the library is captured."""
+    import subprocess
+    import sys
+    subprocess.run([sys.executable, "-c", FIRST_CALL], check=True, timeout=300)
+
+
+def test_profile_names_the_kernels(ra):
+    x = make([300, 200], [60, 1], 4, 2, 64, 16, torch.bfloat16, seed=17)
+    ra.profile_reset()
+    ra.profile_enable(True)
+    try:
+        _run(ra, x, True)
+    finally:
+        ra.profile_enable(False)
+    counts = {k: v[0] for k, v in ra.profile_read().items()}
+    ra.profile_reset()
+    assert [counts["paged_" + k] for k in ("rows_kernel", "tiles_kernel", "join_kernel", "plan_kernel")] == [1, 1, 1, 0]
+
+
+def test_refusals_on_the_gpu(ra):
+    """Arguments that do not belong together, refused before a launch."""
+    x = make([33], [2], 4, 2, 64, 16, torch.bfloat16, seed=18)
+    a = {n: x[n].cuda() for n in ("q", "k_cache", "v_cache", "table", "seq_lens", "cu_q")}
+
+    def call(**kw):
+        b = dict(a, **kw)
+        extra = {k: b.pop(k) for k in list(b) if k not in a}
+        return ra.paged_attn_fwd(b["q"], b["k_cache"], b["v_cache"], b["table"], b["seq_lens"], b["cu_q"], True, **extra)
+
+    for wrong, kind in (
+            (dict(q=a["q"].float()), TypeError), (dict(k_cache=a["k_cache"].half()), TypeError),
+            (dict(v_cache=a["v_cache"][:-1]), ValueError), (dict(seq_lens=a["seq_lens"].long()), TypeError),
+            (dict(cu_q=a["cu_q"][:1]), ValueError), (dict(table=a["table"].cpu()), ValueError),
+            (dict(q=a["q"][:, :3]), ValueError), (dict(o=torch.empty_like(a["q"])[:1]), ValueError),
+            (dict(lse=torch.empty(2, 4, device="cuda")), ValueError), (dict(scale=-1.0), ra.RingAttnError),
+            (dict(q=a["q"].transpose(1, 2).contiguous().transpose(1, 2)), ValueError),
+            (dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda")), ra.RingAttnError)):
+        with pytest.raises(kind):
+            call(**wrong)
+    k = a["q"][:, :2]
+    with pytest.raises(ValueError):
+        ra.paged_kv_append(k, k[:1], a["k_cache"], a["v_cache"], _i32([0, 1]))
+    with pytest.raises(ra.RingAttnError):
+        ra.paged_kv_append(k, k, a["k_cache"][:, :12], a["v_cache"][:, :12], _i32([0, 1]))
+    with pytest.raises(ValueError):
+        ra.paged_kv_plan(_i32([0]), _i32([1, 1]), a["table"], _i32([0]), _i32([1, 0]), 16, 1)
+    assert ra.check_status() == ra.RA_OK
+
+
 # ---------------------------------------------------------------------------
 # Together
 # ---------------------------------------------------------------------------
