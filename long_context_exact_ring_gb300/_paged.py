@@ -4,6 +4,7 @@ tensors, on that device's current stream unless ``stream`` names one)."""
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -162,6 +163,7 @@ def paged_kv_append(k, v, k_cache, v_cache, slots, *, stream=None):
     return k_cache, v_cache
 
 
+@functools.lru_cache(maxsize=256)
 def paged_attn_workspace_size(n: int, tokens: int, H: int, H_kv: int, d: int) -> int:
     return int(load_library().paged_attn_workspace_size(n, tokens, H, H_kv, d))
 
@@ -189,23 +191,32 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_q, causal: boo
     pool = (num_pages, page_size, H_kv, d)
     table, n, max_pages, stride = _table(block_table, dev)
     lib = load_library()
+    # what is made here needs no check
     own = []
+    q_at = _elems(q, "q", dtype, shape, dev)
     if o is None:
         o = torch.empty_like(q)
         own.append(o)
+        o_at = (o.data_ptr(), q_at[1] and _LL2(o.stride(0), o.stride(1)))
+    else:
+        o_at = _elems(o, "o", dtype, shape, dev)
     if lse is None:
         lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
         own.append(lse)
+        lse_at = lse.data_ptr()
+    else:
+        lse_at = _whole(lse, "lse", torch.float32, (H, T), dev)
     if workspace is None:
-        workspace = torch.empty(max(lib.paged_attn_workspace_size(n, T, H, H_kv, d), 1), dtype=torch.uint8,
-                                device=q.device)
+        ws_bytes = paged_attn_workspace_size(n, T, H, H_kv, d)
+        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=q.device)
         own.append(workspace)
-    _call(dev, stream, own, "paged_attn_fwd", lib.paged_attn_fwd, *_elems(q, "q", dtype, shape, dev),
+        ws_at = workspace.data_ptr()
+    else:
+        ws_at = _whole(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
+        ws_bytes = workspace.numel()
+    _call(dev, stream, own, "paged_attn_fwd", lib.paged_attn_fwd, *q_at,
           *_elems(k_cache, "k_cache", dtype, pool, dev), *_elems(v_cache, "v_cache", dtype, pool, dev), table, stride,
-          _whole(seq_lens, "seq_lens", _I32, (n,), dev), _whole(cu_q, "cu_q", _I32, (n + 1,), dev),
-          *_elems(o, "o", dtype, shape, dev), _whole(lse, "lse", torch.float32, (H, T), dev), _DTYPES[dtype], n, T, H,
-          H_kv, d, num_pages, page_size, max_pages, T if max_q is None else int(max_q), int(bool(causal)),
-          1.0 / math.sqrt(d) if scale is None else float(scale),
-          _whole(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev),
-          workspace.numel())
+          _whole(seq_lens, "seq_lens", _I32, (n,), dev), _whole(cu_q, "cu_q", _I32, (n + 1,), dev), *o_at, lse_at,
+          _DTYPES[dtype], n, T, H, H_kv, d, num_pages, page_size, max_pages, T if max_q is None else int(max_q),
+          int(bool(causal)), 1.0 / math.sqrt(d) if scale is None else float(scale), ws_at, ws_bytes)
     return o, lse
