@@ -217,7 +217,7 @@ int launch_attn(const ra::paged::AttnParams& p, void* workspace, int max_q, int 
     if (e == cudaSuccess) {
         const int first = run_tiles ? 0 : kBigSlices, last = run_rows ? kBigSlices + 1 : kBigSlices;
         ra::prof::Scope ps(ra::prof::kPagedJoin, s);
-        e = launch_after(true, paged_join_kernel<D, kHalf>, dim3(blocks, last - first), 256, 0, s, p, few, big, blocks,
+        e = launch_after(true, paged_join_kernel<D, kHalf>, dim3(blocks, last - first), kJoinThreads, 0, s, p, few, big, blocks,
                          tp.tok_tile * p.group, first);
         ps.done();
     }

@@ -114,7 +114,9 @@ __device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr)
 // most two unfinished tiles: one that it takes over from the block before
 // (part 0) and one that it leaves to the block behind (part 1).
 // ---------------------------------------------------------------------------
-constexpr int kMaxBlocks = 256;    // and threads of a block of paged_join_kernel
+constexpr int kMaxBlocks = 160;    // one to an SM: 152
+constexpr int kJoinThreads = 256;
+static_assert(kMaxBlocks <= kJoinThreads, "a thread of the join to each block");
 
 struct PartInfo {
     int req;        // -1: no such part
@@ -185,7 +187,7 @@ __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct JoinShared {
-    int slot[kMaxBlocks], base[kMaxBlocks / 32], end;
+    int slot[kMaxBlocks], base[kJoinThreads / 32], end;
     float m[kMaxBlocks][16], l[kMaxBlocks][16];
 };
 
@@ -203,7 +205,7 @@ __device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& 
     const int tid = threadIdx.x;
     // the parts: this block's, then those of the blocks behind it up to the
     // one that ends the tile; a block without work has none
-    if (tid == 0) s.end = kMaxBlocks;
+    if (tid == 0) s.end = kJoinThreads;
     __syncthreads();
     const int next = b + 1 + tid;
     PartInfo other;
@@ -216,21 +218,21 @@ __device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& 
     if (tid % 32 == 0) s.base[tid / 32] = __popc(votes);
     __syncthreads();
     int at = 1 + __popc(votes & ((1u << tid % 32) - 1u)), parts = 1;
-    for (int w = 0; w < kMaxBlocks / 32; ++w) {
+    for (int w = 0; w < kJoinThreads / 32; ++w) {
         at += w < tid / 32 ? s.base[w] : 0;
         parts += s.base[w];
     }
     if (mine) s.slot[at] = 2 * next;
     if (tid == 0) s.slot[0] = 2 * b + 1;
     __syncthreads();
-    for (int x = tid; x < parts * 16; x += 256) {
+    for (int x = tid; x < parts * 16; x += kJoinThreads) {
         const float* ml = ws.ml + (size_t)s.slot[x / 16] * 2 * kTileRows + slice * 16 + x % 16;
         s.m[x / 16][x % 16] = ml[0];
         s.l[x / 16][x % 16] = ml[kTileRows];
     }
     __syncthreads();
 
-    constexpr int kPer = 16 * D / 256;
+    constexpr int kPer = 16 * D / kJoinThreads;
     const int lane_row = tid % 16, row = slice * 16 + lane_row, col = tid / 16 * kPer;
     const Request r = load_request(p, info.req);
     const int packed = info.row0 + row / kHalfRows * used + row % kHalfRows;
@@ -265,7 +267,7 @@ constexpr int kBigSlices = kBigTile / 16;
 
 // Slices 0 .. kBigSlices - 1 of the large tiles, then the small ones.
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(kJoinThreads)
 paged_join_kernel(const AttnParams p, const Workspace rows, const Workspace big, int blocks, int used, int first_slice)
 {
     __shared__ JoinShared s;
