@@ -358,16 +358,21 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
                     for (int y = 0; y < 4; ++y) st.acc[x][y] *= alpha[y >> 1];
             }
-            // Weights rounded to the operand type (half a step of 2^-9 or
-            // 2^-12 each); l sums them unrounded.
-            uint32_t pa[kSteps16][4];
+            // Weights rounded to the operand type.  bf16's half step of 2^-9 would
+            // show in O, so what it leaves out is rounded and multiplied too, for 1 %
+            // of a long decode's time; fp16's half step of 2^-12 stays.  l sums the
+            // weights unrounded.
+            uint32_t pa[kSteps16][4], pr[kSteps16][4];
 #pragma unroll
-            for (int z = 0; z < kSteps16; ++z) {
-                pa[z][0] = Op::pack(s[2 * z][0], s[2 * z][1]);
-                pa[z][1] = Op::pack(s[2 * z][2], s[2 * z][3]);
-                pa[z][2] = Op::pack(s[2 * z + 1][0], s[2 * z + 1][1]);
-                pa[z][3] = Op::pack(s[2 * z + 1][2], s[2 * z + 1][3]);
-            }
+            for (int z = 0; z < kSteps16; ++z)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float w0 = s[2 * z + (i >> 1)][2 * (i & 1)], w1 = s[2 * z + (i >> 1)][2 * (i & 1) + 1];
+                    pa[z][i] = Op::pack(w0, w1);
+                    if constexpr (!kHalf)
+                        pr[z][i] = Op::pack(w0 - __uint_as_float(pa[z][i] << 16),
+                                            w1 - __uint_as_float(pa[z][i] & 0xffff0000u));
+                }
 
             // ---- O += P V
             auto load_v = [&](uint32_t (&vb)[4], int z, int x) {
@@ -384,6 +389,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         load_v(vb, z, x);
                         Op::mma(st.acc[2 * x], pa[z], vb[0], vb[1]);
                         Op::mma(st.acc[2 * x + 1], pa[z], vb[2], vb[3]);
+                        if constexpr (!kHalf) {
+                            Op::mma(st.acc[2 * x], pr[z], vb[0], vb[1]);
+                            Op::mma(st.acc[2 * x + 1], pr[z], vb[2], vb[3]);
+                        }
                     }
             } else {
                 // Rows of V behind the last key in use hold anything: cleared.
@@ -416,6 +425,10 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                         if (!odd) {
                             Op::mma(st.acc[2 * x], pa[z], vb[0], vb[1]);
                             Op::mma(st.acc[2 * x + 1], pa[z], vb[2], vb[3]);
+                            if constexpr (!kHalf) {
+                                Op::mma(st.acc[2 * x], pr[z], vb[0], vb[1]);
+                                Op::mma(st.acc[2 * x + 1], pr[z], vb[2], vb[3]);
+                            }
                             continue;
                         }
 #pragma unroll 1
@@ -424,10 +437,18 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
                             const uint32_t lower = key < 8 ? sel : 0u, upper = key < 8 ? 0u : sel;
                             const uint32_t one[4] = {pa[z][0] & lower, pa[z][1] & lower, pa[z][2] & upper,
                                                      pa[z][3] & upper};
+                            uint32_t rest[4] = {};
+                            if constexpr (!kHalf) {
+                                rest[0] = pr[z][0] & lower;
+                                rest[1] = pr[z][1] & lower;
+                                rest[2] = pr[z][2] & upper;
+                                rest[3] = pr[z][3] & upper;
+                            }
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 float d[4] = {0.f, 0.f, 0.f, 0.f};
                                 Op::mma(d, one, vb[2 * y] & lower, vb[2 * y + 1] & upper);
+                                if constexpr (!kHalf) Op::mma(d, rest, vb[2 * y] & lower, vb[2 * y + 1] & upper);
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
                                     if (key16 + key <= lim[e >> 1]) st.acc[2 * x + y][e] += d[e];
