@@ -374,7 +374,8 @@ typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
  * the slots is not granted, and from the first one for whose pages the stack
  * is too short no request that needs pages is.  A request that is not
  * granted keeps its length, its pages and its tokens' places in cu_q; try it
- * again when there are pages.
+ * again when there are pages.  (Its rows of paged_attn_fwd in this step are
+ * those of the last tokens that its cache holds: discard them.)
  * seq_lens_out may be seq_lens and counts_out may be counts (a loop's state,
  * updated in place); otherwise buffers do not overlap.  Where they are not
  * updated in place the call can be repeated with the same result.
@@ -406,8 +407,8 @@ int paged_kv_append(const void *k, const long long *k_strides, const void *v,
 size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d);
 
 /*
- * Attention of new tokens over their requests' contexts, exactly as
- * ring_attn_fwd_gqa computes it for the last rows of each context.
+ * Attention of new tokens over their requests' contexts: what
+ * ring_attn_fwd_gqa gives for the last rows of each context.
  *   q            [tokens, H, d] the new tokens of all requests, one request
  *                after the other; request i's are rows cu_q[i] .. cu_q[i+1].
  *                Rows are placed by q_strides {token, head}; NULL =
@@ -423,12 +424,14 @@ size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d);
  *                identity of attn_merge_partials.
  *   scale        finite and above 0.
  *   max_q        an upper bound of the new tokens of one request, for the
- *                choice of kernels only: results do not depend on it.
+ *                choice of kernels only: a wrong one costs time, and results
+ *                differ by rounding at most.
  *   dtype        RA_BF16 or RA_FP16, of q, the pools and o.
  *   max_pages    as in paged_kv_plan: max_pages * page_size at most 2^30.
  *   H / H_kv     a whole number up to 128 (more: RA_ERR_UNSUPPORTED).
- *   workspace    paged_attn_workspace_size bytes, 256-byte aligned, of any
- *                contents; calls that may run at the same time need one each.
+ *   workspace    paged_attn_workspace_size bytes (up to 46 MB), 256-byte
+ *                aligned, of any contents; calls that may run at the same
+ *                time need one each.
  * Keys behind a row's last one do not reach it, whatever they hold.
  */
 int paged_attn_fwd(const void *q, const long long *q_strides, const void *k_cache,

@@ -14,8 +14,9 @@ from ._binding import _check, load_library
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _LL2, _LL3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
 _I32 = torch.int32
-_current_device = torch._C._cuda_getDevice
-_current_stream = torch._C._cuda_getCurrentRawStream     # a stream's handle, without a Stream object
+# A stream's handle without a Stream object; absent from a torch without CUDA.
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _refuse(t, name, dtype, shape, device, rows):
