@@ -127,7 +127,7 @@ struct PartInfo {
 struct Workspace {
     PartInfo* info;   // [blocks][2]
     float* ml;        // [blocks][2][2][tile rows] reference and sum of the exponentials
-    float* acc;       // [blocks][2][D / 4][tile rows][4] sums, not normalized
+    float* acc;       // [blocks][2][tile rows x D] sums, not normalized (part_columns)
 };
 
 // Workspace of a kernel with tiles of `rows` packed rows.
@@ -145,11 +145,14 @@ __host__ __device__ inline Workspace workspace(void* base, int rows)
     return w;
 }
 
-// Where four columns of a part's row lie: the rows of a tile are neighbours, so
-// that lanes which hold a row each write whole lines.
-__device__ __forceinline__ float4* part_columns(const Workspace& ws, int slot, int tile_rows, int D, int row, int col)
+// Where four columns of a part's row lie.  In a large tile the rows are
+// neighbours, as a lane that writes holds a row; in a small one the columns, as
+// a warp holds a row: either way a warp writes whole lines.
+template <int kTileRows>
+__device__ __forceinline__ float4* part_columns(const Workspace& ws, int slot, int D, int row, int col)
 {
-    return reinterpret_cast<float4*>(ws.acc) + ((size_t)slot * (D / 4) + col / 4) * tile_rows + row;
+    float4* part = reinterpret_cast<float4*>(ws.acc) + (size_t)slot * kTileRows * (D / 4);
+    return part + (kTileRows == 16 ? row * (D / 4) + col / 4 : col / 4 * kTileRows + row);
 }
 
 // Which requests a kernel serves: those with more than `above` and at most
@@ -173,7 +176,8 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Request& r,
 #pragma unroll
     for (int c = 0; c < kPer / 2; ++c) pk[c] = Op::pack(out[2 * c] * inv, out[2 * c + 1] * inv);
     if constexpr (kPer == 8) *reinterpret_cast<uint4*>(dst) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-    else *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+    else if constexpr (kPer == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(pk[0], pk[1]);
+    else *reinterpret_cast<uint32_t*>(dst) = pk[0];
     if (col == 0)
         p.lse[(long long)head * p.tokens + r.first + tok] =
             m == -INFINITY ? -INFINITY : (m - shift + log2f(l)) * 0.69314718055994531f;
@@ -233,7 +237,9 @@ __device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& 
     __syncthreads();
 
     constexpr int kPer = 16 * D / kJoinThreads;
-    const int lane_row = tid % 16, row = slice * 16 + lane_row, col = tid / 16 * kPer;
+    // as the parts lie: columns are neighbours in a small tile, rows in a large one
+    const int lane_row = kTileRows == 16 ? tid / 16 : tid % 16, row = slice * 16 + lane_row;
+    const int col = (kTileRows == 16 ? tid % 16 : tid / 16) * kPer;
     const Request r = load_request(p, info.req);
     const int packed = info.row0 + row / kHalfRows * used + row % kHalfRows;
     if (row % kHalfRows >= used || packed >= r.q * p.group) return;
@@ -248,7 +254,7 @@ __device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& 
             l += w * s.l[x][lane_row];
 #pragma unroll
             for (int c = 0; c < kPer; c += 4) {
-                const float4 v = *part_columns(ws, s.slot[x], kTileRows, D, row, col + c);
+                const float4 v = *part_columns<kTileRows>(ws, s.slot[x], D, row, col + c);
                 out[c] += w * v.x;
                 out[c + 1] += w * v.y;
                 out[c + 2] += w * v.z;

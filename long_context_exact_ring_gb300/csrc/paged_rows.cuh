@@ -26,9 +26,9 @@ struct Cfg {
     static constexpr int kBoxBytes = 64 * kUnit * 2;
     static constexpr int kTileBytes = kUnit * D * 2;               // K (or V) of a unit
     static constexpr int kStages = 3;
-    static constexpr int kStateBytes = kRows * D * 4 + 2 * kRows * 4;
-    static constexpr int kOffMerge = 2 * kStages * kTileBytes;
-    static constexpr int kOffBar = kOffMerge + kWarps / 2 * kStateBytes;
+    static constexpr int kOffSums = 2 * kStages * kTileBytes;      // [warp][8 rows][D] of half a tile
+    static constexpr int kOffStat = kOffSums + kWarps * 8 * D * 4; // [2][warp][8 rows] references, sums
+    static constexpr int kOffBar = kOffStat + 2 * kWarps * 8 * 4;
     static constexpr int kSmemBytes = kOffBar + 256 + 1024;        // + alignment slack
 };
 
@@ -118,8 +118,8 @@ struct RowsParams {
 // long context keeps all SMs reading as well as many short ones do.  One warp
 // copies K and V, page by page (TMA), as far ahead as there are stages, into
 // the block's next tiles too; eight warps take an eighth of a unit's keys and keep a
-// softmax state each.  The states are merged in pairs at the end of a tile, or
-// of the block's part of it, and parts by paged_join_kernel.
+// softmax state each.  The states are merged at the end of a tile, or of the
+// block's part of it, and parts by paged_join_kernel.
 //
 // Bound by HBM: K and V are read once per 16 packed rows.  (mma.sync: 16 rows
 // leave the tcgen05 tile of 128 empty, and the products are not the bound.)
@@ -147,8 +147,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     const uint32_t bar0 = base + C::kOffBar;
     auto bar_full = [&](int s) { return bar0 + 8u * s; };                          // copies -> products
     auto bar_empty = [&](int s) { return bar0 + 8u * (C::kStages + s); };          // products -> copies
-    auto bar_state = [&](int w) { return bar0 + 8u * (2 * C::kStages + w); };      // warp w's state written
-    auto bar_read = [&](int w) { return bar0 + 8u * (2 * C::kStages + 8 + w); };   // buffer w's last state read
+    const uint32_t bar_given = bar0 + 8u * (2 * C::kStages);                       // every warp's state is written
+    const uint32_t bar_taken = bar0 + 8u * (2 * C::kStages + 1);                   // and read
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     let_next_start();
 
@@ -175,8 +175,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             mbar_init(bar_full(s), 1);
             mbar_init(bar_empty(s), kWarps);
         }
-        for (int w = 0; w < kWarps; ++w) mbar_init(bar_state(w), 1);
-        for (int w = 0; w < kWarps / 2; ++w) mbar_init(bar_read(w), 1);
+        mbar_init(bar_given, kWarps);
+        mbar_init(bar_taken, kWarps);
         fence_mbar_init();
     }
     __syncthreads();
@@ -263,7 +263,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
     };
     uint32_t qa[D / 16][4];
     load_q(qa);
-    uint32_t n = 0, piece = 0;
+    uint32_t n = 0, merges = 0;
     bool ok = true, more = true;
     while (ok && more) {
         const int row0 = walk.row0(), rows = walk.rows(), kvh = walk.kvh(), keys = walk.keys();
@@ -469,95 +469,74 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
         more = walk.next();
         if (more) load_q(qa);
 
-        // ---- merge the eight warps: 4-7 into 0-3, 2-3 into 0-1, 1 into 0.  Warp
-        // w writes buffer w & 3, which its reader has written or read before;
-        // warps 4-7 wait for the last reader of the piece before.
+        // ---- merge the eight warps, eight rows at a time: every warp writes
+        // the rows in use of its state, then warp w sums row w over all of them.
+        // Columns are swizzled by row, against bank conflicts.
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 1);
             st.l[e] += __shfl_xor_sync(0xffffffffu, st.l[e], 2);
         }
-#pragma unroll 1
-        for (int half = kWarps / 2; half > 0; half >>= 1) {
-            if (w >= 2 * half) continue;
-            const bool give = w >= half;
-            const int from = give ? w : w + half;       // the warp whose state is handed over
-            float* state = reinterpret_cast<float*>(gbase + C::kOffMerge + (from & 3) * C::kStateBytes);
-            float4* acc = reinterpret_cast<float4*>(state) + lane;
-            float* ml = state + kRows * D;
-            if (give) {
-                if (half == kWarps / 2 && !(ok = wait_all(bar_read(w & 3), piece + 1u))) break;
-#pragma unroll
-                for (int x = 0; x < D / 8; ++x)
-                    acc[32 * x] = make_float4(st.acc[x][0], st.acc[x][1], st.acc[x][2], st.acc[x][3]);
-                if (t4 == 0) {
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        ml[g + 8 * e] = st.m[e];
-                        ml[kRows + g + 8 * e] = st.l[e];
-                    }
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar_state(w));
-            } else {
-                if (!(ok = wait_all(bar_state(from), piece))) break;
-                float mine[2], other[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float mo = ml[g + 8 * e];
-                    const float m = max_nan(st.m[e], mo);
-                    // a state without keys is all 0 and adds nothing
-                    mine[e] = st.m[e] == -INFINITY ? 0.f : ex2_approx(st.m[e] - m);
-                    other[e] = mo == -INFINITY ? 0.f : ex2_approx(mo - m);
-                    st.m[e] = m;
-                    st.l[e] = st.l[e] * mine[e] + ml[kRows + g + 8 * e] * other[e];
-                }
-#pragma unroll
-                for (int x = 0; x < D / 8; ++x) {
-                    const float4 v = acc[32 * x];
-                    st.acc[x][0] = st.acc[x][0] * mine[0] + v.x * other[0];
-                    st.acc[x][1] = st.acc[x][1] * mine[0] + v.y * other[0];
-                    st.acc[x][2] = st.acc[x][2] * mine[1] + v.z * other[1];
-                    st.acc[x][3] = st.acc[x][3] * mine[1] + v.w * other[1];
-                }
-                // buffers 0 and 1 are last read by warp 0, as 4's and 1's
-                // state, 2 by warp 0 as 2's, 3 by warp 1 as 3's
-                __syncwarp();
-                if (lane == 0 && (from == 4 || from < 4)) mbar_arrive(bar_read(from & 3));
-            }
-        }
-        if (!ok) break;
-        ++piece;
-        if (w != 0) continue;
+        float* sums = reinterpret_cast<float*>(gbase + C::kOffSums);
+        float* stat = reinterpret_cast<float*>(gbase + C::kOffStat);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int row = g + 8 * e;
-            if (whole) {
-                if (row >= rows) continue;
-                // no key, or none with a weight: O = 0, LSE = -inf
-                const float inv = st.m[e] == -INFINITY ? 0.f : 1.f / st.l[e];
-                const int tok = (row0 + row) / p.group, head = kvh * p.group + (row0 + row - tok * p.group);
-                uint16_t* dst = p.o + (long long)(r.first + tok) * p.o_tok + (long long)head * p.o_head + 2 * t4;
+            if (8 * e >= rows) break;
+            if (!(ok = wait_all(bar_taken, merges + 1u))) break;
+            if (8 * e + g < rows) {
+                float* to = sums + (w * 8 + g) * D;
 #pragma unroll
                 for (int x = 0; x < D / 8; ++x)
-                    *reinterpret_cast<uint32_t*>(dst + 8 * x) =
-                        Op::pack(st.acc[x][2 * e] * inv, st.acc[x][2 * e + 1] * inv);
-                if (t4 == 0)
-                    p.lse[(long long)head * p.tokens + r.first + tok] =
-                        st.m[e] == -INFINITY ? -INFINITY
-                                             : (st.m[e] - Op::kShift + log2f(st.l[e])) * 0.69314718055994531f;
-            } else {
-#pragma unroll
-                for (int x = 0; x < D / 8; ++x)
-                    reinterpret_cast<float2*>(part_columns(rp.ws, slot, kRows, D, row, 8 * x + 2 * t4))[t4 & 1] =
+                    *reinterpret_cast<float2*>(to + ((8 * x + 2 * t4) ^ (g << 3))) =
                         make_float2(st.acc[x][2 * e], st.acc[x][2 * e + 1]);
                 if (t4 == 0) {
-                    rp.ws.ml[slot * 2 * kRows + row] = st.m[e];
-                    rp.ws.ml[slot * 2 * kRows + kRows + row] = st.l[e];
+                    stat[w * 8 + g] = st.m[e];
+                    stat[kWarps * 8 + w * 8 + g] = st.l[e];
                 }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_given);
+            if (!(ok = wait_all(bar_given, merges))) break;
+            const int row = 8 * e + w;
+            if (row < rows) {
+                constexpr int kPer = D / 32;          // columns of a lane
+                float m = -INFINITY, l = 0.f, out[kPer];
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) m = max_nan(m, stat[x * 8 + w]);
+#pragma unroll
+                for (int c = 0; c < kPer; ++c) out[c] = 0.f;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) {
+                    const float mx = stat[x * 8 + w];
+                    // a state without keys is all 0 and adds nothing
+                    const float f = mx == -INFINITY ? 0.f : ex2_approx(mx - m);
+                    l += f * stat[kWarps * 8 + x * 8 + w];
+                    const float* from = sums + (x * 8 + w) * D + ((kPer * lane) ^ (w << 3));
+                    float v[kPer];
+                    if constexpr (kPer == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(from);
+                    else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(from);
+#pragma unroll
+                    for (int c = 0; c < kPer; ++c) out[c] += f * v[c];
+                }
+                const int col = kPer * lane;
+                if (whole) {
+                    store_row<kPer, kHalf>(p, r, kvh, row0 + row, col, out, m, l, Op::kShift);
+                } else {
+                    float* to = reinterpret_cast<float*>(part_columns<kRows>(rp.ws, slot, D, row, col)) + (col & 3);
+                    if constexpr (kPer == 4) *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(out);
+                    else *reinterpret_cast<float2*>(to) = *reinterpret_cast<const float2*>(out);
+                    if (lane == 0) {
+                        rp.ws.ml[slot * 2 * kRows + row] = m;
+                        rp.ws.ml[slot * 2 * kRows + kRows + row] = l;
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_taken);
+            ++merges;
         }
-        if (!whole && lane == 0) rp.ws.info[slot] = info;
+        if (!ok) break;
+        if (!whole && w == 0 && lane == 0) rp.ws.info[slot] = info;
     }
 }
 

@@ -91,6 +91,11 @@ struct TileParams {
 // tokens, d 64: 319 us without it, 254 with 2, 241 with 3 or 4, 254 with 6.
 constexpr int kExtra = 3;
 
+// The least share of a block, in key tiles: a little work on few blocks has
+// fewer parts to write and to join (17 tokens over 19K, 12 heads on one: 66 us
+// without it, 42 with 5 or 8; 509 tokens on their own: 36, 38 and 43 us).
+constexpr int kMinShare = 5;
+
 // A block's place in its share: key tiles [k0, k1) of a tile, of `total`.
 struct Walk {
     const TileParams& p;
@@ -261,7 +266,9 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
     long long mine = 0, total;
     for (int i = i0; i < i1; ++i) mine += Walk::cost(p, i);
     const long long before = block_exclusive_sum(mine, s_scratch, &total);
-    const Share share = share_of(total, G, b);
+    const int sharing = total >= (long long)G * kMinShare ? G : max(1, (int)total / kMinShare);
+    Share share{0, 0};
+    if (b < sharing) share = share_of(total, sharing, b);
     const long long start = share.start;
     if (tid < 2) p.ws.info[2 * b + tid].req = -1;
     if (share.count == 0) {
@@ -757,7 +764,7 @@ paged_tiles_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_const
                         tmem_ld_wait(o);
 #pragma unroll
                         for (int x = 0; x < 8; ++x)
-                            *part_columns(p.ws, slot, kTileRows, D, u * kBM + row, 32 * c4 + 4 * x) = make_float4(
+                            *part_columns<kTileRows>(p.ws, slot, D, u * kBM + row, 32 * c4 + 4 * x) = make_float4(
                                 __uint_as_float(o[4 * x]), __uint_as_float(o[4 * x + 1]),
                                 __uint_as_float(o[4 * x + 2]), __uint_as_float(o[4 * x + 3]));
                     }
