@@ -358,9 +358,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
                     for (int y = 0; y < 4; ++y) st.acc[x][y] *= alpha[y >> 1];
             }
-            // Weights rounded to the operand type.  bf16's half step of 2^-9 would
+            // Weights rounded to the operand type.  bf16's half step of 2^-8 would
             // show in O, so what it leaves out is rounded and multiplied too, for 1 %
-            // of a long decode's time; fp16's half step of 2^-12 stays.  l sums the
+            // of a long decode's time; fp16's half step of 2^-11 stays.  l sums the
             // weights unrounded.
             uint32_t pa[kSteps16][4], pr[kSteps16][4];
 #pragma unroll
