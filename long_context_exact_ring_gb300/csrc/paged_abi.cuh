@@ -215,7 +215,7 @@ int launch_attn(const ra::paged::AttnParams& p, void* workspace, int max_q, int 
     if (run_rows) e = launch_rows<D, kHalf>(maps, rp, blocks, s);
     if (run_tiles && e == cudaSuccess) e = launch_tiles<D, kHalf>(run_rows, maps, tp, blocks, s);
     if (e == cudaSuccess) {
-        const int first = run_tiles ? 0 : kBigSlices, last = run_rows ? kBigSlices + 1 : kBigSlices;
+        const int first = run_tiles ? 0 : kBigSlices, last = kBigSlices + (run_rows ? kRowsSlices : 0);
         ra::prof::Scope ps(ra::prof::kPagedJoin, s);
         e = launch_after(true, paged_join_kernel<D, kHalf>, dim3(blocks, last - first), kJoinThreads, 0, s, p, few, big, blocks,
                          tp.tok_tile * p.group, first);

@@ -190,25 +190,27 @@ __device__ __forceinline__ void store_row(const AttnParams& p, const Request& r,
 __device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// The two kernels' tiles (paged_rows_kernel's, paged_tiles_kernel's): rows of
+// a tile, rows of its halves, shift of the reference; slices of a tile that
+// are joined by a block each.
+constexpr int kRowsTile = 16, kBigTile = 256, kBigHalf = 128;
+template <bool kHalf> constexpr float kBigShift = kHalf ? 7.f : 0.f;
+constexpr int kRowsSlices = 4, kBigSlices = 16;
+
 struct JoinShared {
     int slot[kMaxBlocks], base[kJoinThreads / 32], end;
-    float m[kMaxBlocks][16], l[kMaxBlocks][16];
+    alignas(16) float m[kMaxBlocks][16];
+    float l[kMaxBlocks][16];
 };
 
-// Joins the parts of a tile that several blocks had a share of: the block
-// that began it, then those behind it, in order -- the sum does not depend
-// on which finished first.  A tile's rows come in halves of kHalfRows, of
-// which the first `used` hold packed rows.  Joins rows 16 slice .. 16 slice +
-// 15 of the tile that block b began and did not finish.
-template <int D, bool kHalf, int kTileRows, int kHalfRows>
-__device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& ws, int blocks, int b, int slice,
-                                          int used, float shift, JoinShared& s)
+// The parts of the tile that block b began and did not finish: this block's,
+// then those of the blocks behind it up to the one that ends the tile (a block
+// without work has none), with the references and sums of kRows of its rows.
+// Returns their number.
+template <int kTileRows, int kRows>
+__device__ __forceinline__ int list_parts(const Workspace& ws, int blocks, int b, int row0, JoinShared& s)
 {
-    const PartInfo info = ws.info[2 * b + 1];
-    if (info.req < 0) return;
     const int tid = threadIdx.x;
-    // the parts: this block's, then those of the blocks behind it up to the
-    // one that ends the tile; a block without work has none
     if (tid == 0) s.end = kJoinThreads;
     __syncthreads();
     const int next = b + 1 + tid;
@@ -229,20 +231,31 @@ __device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& 
     if (mine) s.slot[at] = 2 * next;
     if (tid == 0) s.slot[0] = 2 * b + 1;
     __syncthreads();
-    for (int x = tid; x < parts * 16; x += kJoinThreads) {
-        const float* ml = ws.ml + (size_t)s.slot[x / 16] * 2 * kTileRows + slice * 16 + x % 16;
-        s.m[x / 16][x % 16] = ml[0];
-        s.l[x / 16][x % 16] = ml[kTileRows];
+    for (int x = tid; x < parts * kRows; x += kJoinThreads) {
+        const float* ml = ws.ml + (size_t)s.slot[x / kRows] * 2 * kTileRows + row0 + x % kRows;
+        s.m[x / kRows][x % kRows] = ml[0];
+        s.l[x / kRows][x % kRows] = ml[kTileRows];
     }
     __syncthreads();
+    return parts;
+}
 
+// Joins rows 16 slice .. 16 slice + 15 of a large tile; the parts are added in
+// order, so the sum does not depend on which finished first.  A tile's rows
+// come in halves of kBigHalf, of which the first `used` hold packed rows.
+template <int D, bool kHalf>
+__device__ __forceinline__ void join_big(const AttnParams& p, const Workspace& ws, int blocks, int b, int slice,
+                                         int used, JoinShared& s)
+{
+    const PartInfo info = ws.info[2 * b + 1];
+    if (info.req < 0) return;
+    const int parts = list_parts<kBigTile, 16>(ws, blocks, b, 16 * slice, s);
     constexpr int kPer = 16 * D / kJoinThreads;
-    // as the parts lie: columns are neighbours in a small tile, rows in a large one
-    const int lane_row = kTileRows == 16 ? tid / 16 : tid % 16, row = slice * 16 + lane_row;
-    const int col = (kTileRows == 16 ? tid % 16 : tid / 16) * kPer;
+    // as the parts lie: rows are neighbours
+    const int tid = threadIdx.x, lane_row = tid % 16, row = slice * 16 + lane_row, col = tid / 16 * kPer;
     const Request r = load_request(p, info.req);
-    const int packed = info.row0 + row / kHalfRows * used + row % kHalfRows;
-    if (row % kHalfRows >= used || packed >= r.q * p.group) return;
+    const int packed = info.row0 + row / kBigHalf * used + row % kBigHalf;
+    if (row % kBigHalf >= used || packed >= r.q * p.group) return;
     float m = -INFINITY, l = 0.f, out[kPer];
     for (int x = 0; x < parts; ++x) m = max_nan(m, s.m[x][lane_row]);
 #pragma unroll
@@ -254,7 +267,7 @@ __device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& 
             l += w * s.l[x][lane_row];
 #pragma unroll
             for (int c = 0; c < kPer; c += 4) {
-                const float4 v = *part_columns<kTileRows>(ws, s.slot[x], D, row, col + c);
+                const float4 v = *part_columns<kBigTile>(ws, s.slot[x], D, row, col + c);
                 out[c] += w * v.x;
                 out[c + 1] += w * v.y;
                 out[c + 2] += w * v.z;
@@ -262,27 +275,73 @@ __device__ __forceinline__ void join_part(const AttnParams& p, const Workspace& 
             }
         }
     }
-    store_row<kPer, kHalf>(p, r, info.kvh, packed, col, out, m, l, shift);
+    store_row<kPer, kHalf>(p, r, info.kvh, packed, col, out, m, l, kBigShift<kHalf>);
 }
 
-// The two kernels' tiles (paged_rows_kernel's, paged_tiles_kernel's): rows of
-// a tile, rows of its halves, shift of the reference.
-constexpr int kRowsTile = 16, kBigTile = 256, kBigHalf = 128;
-template <bool kHalf> constexpr float kBigShift = kHalf ? 7.f : 0.f;
-constexpr int kBigSlices = kBigTile / 16;
-
-// Slices 0 .. kBigSlices - 1 of the large tiles, then the small ones.
+// Joins rows 4 slice .. 4 slice + 3 of a small tile.  One long context is a few
+// tiles of many parts, and what bounds it is a chain of reads: groups of
+// threads, one float4 to a thread, take the parts in turn, and their sums are
+// added in order.  (8K keys, 28 heads over 4, the whole call: 27.7 us with a
+// block to a tile, 23.7 so.)
 template <int D, bool kHalf>
-__global__ void __launch_bounds__(kJoinThreads)
+__device__ __forceinline__ void join_small(const AttnParams& p, const Workspace& ws, int blocks, int b, int slice,
+                                           JoinShared& s)
+{
+    constexpr int kRows = kRowsTile / kRowsSlices, kThreads = kRows * D / 4, kGroups = kJoinThreads / kThreads;
+    const PartInfo info = ws.info[2 * b + 1];
+    if (info.req < 0) return;
+    const int parts = list_parts<kRowsTile, kRows>(ws, blocks, b, kRows * slice, s);
+    const int group = threadIdx.x / kThreads, t = threadIdx.x % kThreads;
+    // as the parts lie: columns are neighbours
+    const int lane_row = t / (D / 4), row = slice * kRows + lane_row, col = t % (D / 4) * 4;
+    float m = -INFINITY, l = 0.f, out[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < parts; ++x) m = max_nan(m, s.m[x][lane_row]);
+    if (m != -INFINITY) {
+#pragma unroll 4
+        for (int x = group; x < parts; x += kGroups) {
+            const float w = ex2_approx(s.m[x][lane_row] - m);
+            l += w * s.l[x][lane_row];
+            const float4 v = *part_columns<kRowsTile>(ws, s.slot[x], D, row, col);
+            out[0] += w * v.x;
+            out[1] += w * v.y;
+            out[2] += w * v.z;
+            out[3] += w * v.w;
+        }
+    }
+    __syncthreads();    // m and l are free
+    float4* sum = reinterpret_cast<float4*>(s.m);
+    float* total = s.l[0];
+    sum[threadIdx.x] = make_float4(out[0], out[1], out[2], out[3]);
+    total[threadIdx.x] = l;
+    __syncthreads();
+    const Request r = load_request(p, info.req);
+    const int packed = info.row0 + row;
+    if (group > 0 || packed >= r.q * p.group) return;
+#pragma unroll
+    for (int g = 1; g < kGroups; ++g) {
+        const float4 v = sum[g * kThreads + t];
+        l += total[g * kThreads + t];
+        out[0] += v.x;
+        out[1] += v.y;
+        out[2] += v.z;
+        out[3] += v.w;
+    }
+    store_row<4, kHalf>(p, r, info.kvh, packed, col, out, m, l, Operand<kHalf>::kShift);
+}
+
+// Slices 0 .. kBigSlices - 1 of the large tiles, then those of the small ones.
+// Five blocks to an SM leave the registers that four parts in flight take: with
+// eight (the compiler's choice) 10 contexts of up to 69K, 12 heads on one, take
+// 58 us instead of 53, with three 509 tokens over 4K 54 instead of 52.
+template <int D, bool kHalf>
+__global__ void __launch_bounds__(kJoinThreads, 5)
 paged_join_kernel(const AttnParams p, const Workspace rows, const Workspace big, int blocks, int used, int first_slice)
 {
     __shared__ JoinShared s;
     wait_for_previous();
     const int slice = blockIdx.y + first_slice;
-    if (slice == kBigSlices)
-        join_part<D, kHalf, kRowsTile, kRowsTile>(p, rows, blocks, blockIdx.x, 0, kRowsTile, Operand<kHalf>::kShift, s);
-    else
-        join_part<D, kHalf, kBigTile, kBigHalf>(p, big, blocks, blockIdx.x, slice, used, kBigShift<kHalf>, s);
+    if (slice >= kBigSlices) join_small<D, kHalf>(p, rows, blocks, blockIdx.x, slice - kBigSlices, s);
+    else join_big<D, kHalf>(p, big, blocks, blockIdx.x, slice, used, s);
 }
 
 }  // namespace paged
