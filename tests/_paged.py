@@ -92,6 +92,44 @@ def attn_ref(x, causal, scale=None):
     return o, lse, tol_o, tol_lse
 
 
+def attn_ref_causal(x):
+    """attn_ref(x, True) for longer batches: a matrix product for each request
+    and head.  V may hold infinities and NaN."""
+    q, ps = x["q"], x["k_cache"].shape[1]
+    T, H, d = q.shape
+    H_kv = x["k_cache"].shape[2]
+    scale, u = 1.0 / math.sqrt(d), U[q.dtype]
+    o = torch.full((T, H, d), float("nan"), dtype=torch.float64)
+    lse = torch.full((H, T), float("nan"), dtype=torch.float64)
+    tol_o, tol_lse = torch.zeros_like(o), torch.zeros_like(lse)
+    for i, length in enumerate(x["lens"]):
+        c = torch.arange(length)
+        page = x["table"][i].long()[c // ps]
+        k = x["k_cache"][page, c % ps].double()
+        v = x["v_cache"][page, c % ps].double()
+        rows = slice(x["cu"][i], x["cu"][i] + x["news"][i])
+        m = length - x["news"][i] + torch.arange(x["news"][i]) + 1       # keys that a row sees
+        seen = c[None, :] < m[:, None]
+        for h in range(H):
+            j = h // (H // H_kv)
+            qr = q[rows, h].double()
+            s = scale * (qr @ k[:, j].T)
+            b = (scale * (qr.abs() @ k[:, j].abs().T)).where(seen, 0.0).amax(1)
+            most = s.abs().where(seen, 0.0).amax(1)
+            s = s.where(seen, float("-inf"))
+            lse[h, rows] = torch.logsumexp(s, 1)
+            p = torch.softmax(s, 1)
+            finite = torch.where(torch.isfinite(v[:, j]), v[:, j], 0.0)
+            out = p @ finite
+            e = d * 2.0 ** -24 * b + 2.0 ** -23 * (4 * most + 32) + 2.0 ** -22
+            tol_o[rows, h] = u * out.abs() + (u + 2 * e + m * 2.0 ** -23)[:, None] * (p @ finite.abs())
+            tol_lse[h, rows] = e + m * 2.0 ** -24 + 2.0 ** -23 * lse[h, rows].abs()
+            for key, col in (~torch.isfinite(v[:, j])).nonzero().tolist():
+                out[:, col] += torch.where(seen[:, key], p[:, key] * v[key, j, col], 0.0)
+            o[rows, h] = out
+    return o, lse, tol_o, tol_lse
+
+
 def assert_close(got, want, tol, what):
     got = got.detach().cpu().double()
     assert torch.equal(torch.isnan(got), torch.isnan(want)), f"{what}: NaN in other places"

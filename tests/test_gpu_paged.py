@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import workloads
-from _paged import assert_close, attn_ref, make, pages, plan_ref
+from _paged import assert_close, attn_ref, attn_ref_causal, make, pages, plan_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -359,6 +359,25 @@ def test_attn_one_context_over_all_blocks(ra, new, d, page_size):
     for length in (152 * 128 + 1, 152 * 256 - 1):
         x = make([length], [new], 2, 1, d, page_size, torch.float16, seed=new)
         _check(ra, x, True)
+
+
+@pytest.mark.parametrize("d,dtype", [(64, torch.float16), (128, torch.bfloat16)])
+@pytest.mark.parametrize("odd", [None, "inf", "nan"])
+def test_attn_whole_tiles_between_cut_ones(ra, d, dtype, odd):
+    """Prompts of several key tiles, many tiles to a block: those between a
+    share's first and last begin in the middle of their keys.  A value of V that
+    only the later rows see reaches those alone."""
+    lens = [520, 300, 401, 640, 129, 575] * 4
+    x = make(lens, [a - 7 * (i % 3) for i, a in enumerate(lens)], 16, 8, d, 16, dtype, seed=d)
+    for i, a in enumerate(lens if odd else []):
+        key = a * 2 // 3 - i
+        x["v_cache"][x["table"][i, key // 16], key % 16, i % 8, i] = float(odd)
+    o, lse = _run(ra, x, True)
+    assert ra.check_status() == ra.RA_OK
+    o_ref, lse_ref, tol_o, tol_lse = attn_ref_causal(x)
+    assert bool(torch.isfinite(o_ref).all()) == (odd is None)
+    assert_close(o, o_ref, tol_o, "O")
+    assert_close(lse, lse_ref, tol_lse, "LSE")
 
 
 def test_attn_different_strides_for_keys_and_values(ra):
