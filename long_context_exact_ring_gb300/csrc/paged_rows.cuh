@@ -33,8 +33,9 @@ struct Cfg {
 };
 
 // What a tile costs beside its keys, in units: the states of eight warps are
-// merged and the results written, about 3 us against 1.5 us for a unit.  64
-// ragged contexts up to 16K: 365 us without it, 355 with 1, 340 with 2, 343 with 3.
+// merged and the results written, 2 to 3 us against 1.5 us for a unit.  64
+// ragged contexts up to 16K: 342 us without it, 333 with 1, 329 with 2; 64
+// contexts of up to 1153 keys, 32 heads of 64: 120, 88 and 76 us.
 constexpr int kExtra = 2;
 
 // A block's place in its share: units [u0, u1) of kUnit keys of a tile.
@@ -123,8 +124,8 @@ struct RowsParams {
 //
 // Bound by HBM: K and V are read once per 16 packed rows.  (mma.sync: 16 rows
 // leave the tcgen05 tile of 128 empty, and the products are not the bound.)
-// 64 ragged contexts up to 16K, 32 heads over 8, d 128: 333 us, 1.01 of measured
-// copy bandwidth; one context of 128K, 32 heads: 312 us, 1.03; 128 contexts of
+// 64 ragged contexts up to 16K, 32 heads over 8, d 128: 330 us, 1.01 of measured
+// copy bandwidth; one context of 128K, 32 heads: 305 to 315 us, 1.02 to 1.05; 128 contexts of
 // 8K, 16 heads over 2, d 64: 0.94.  A lone short context (777 keys) takes 8 us,
 // a chain of latencies: lengths, page numbers, keys, merge.
 template <int D, bool kHalf>

@@ -28,9 +28,10 @@
 // Bound, at d 128, by the softmax and its tile's two products taking turns (of
 // 2650 cycles a key tile, 1400 and 1250; the tensor core is at work for 2050 of
 // them), at d 64 by the softmax warps' instructions.  2048 tokens at the end of
-// 64K, 32 heads over 8: 1.64 us a key tile, 1550 TFLOP/s (0.80 of measured) at d
-// 128, 1.32 us at d 64.  Short pieces cost 5 to 6 us beside their keys (kExtra).
-// Blocks of one key/value head read its keys at about the same time, from L2.
+// 64K, 32 heads over 8: 1.53 us a key tile, 1670 TFLOP/s (0.85 of measured) at d
+// 128, 1.30 us at d 64.  Short pieces cost 5 to 6 us beside their keys (kExtra).
+// Blocks of one key/value head read its keys at the same time, from L2 (see
+// Walk::key_tile).
 #pragma once
 
 #include <new>
@@ -87,7 +88,7 @@ struct TileParams {
 
 // What a tile costs beside its key tiles, in key tiles: Q has to arrive, the
 // pipeline to fill and to drain, and the results to be written, 5 to 6 us
-// against 1.5 to 1.7 us for a key tile.  40 requests with 5 chunks of up to 1024
+// against 1.3 to 1.6 us for a key tile.  40 requests with 5 chunks of up to 1024
 // tokens, d 64: 319 us without it, 254 with 2, 241 with 3 or 4, 254 with 6.
 constexpr int kExtra = 3;
 
