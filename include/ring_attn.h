@@ -352,7 +352,7 @@ typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
 
 /*
  * The bookkeeping of one step, for n requests (n <= 8192, else
- * RA_ERR_UNSUPPORTED).
+ * RA_ERR_UNSUPPORTED; 0 writes cu_q[0], slots and counts_out).
  *   seq_lens     [n] int32 tokens in the cache.
  *   new_lens     [n] int32 tokens to add; 0 leaves a request as it is, a
  *                negative value ends it and gives its pages back.
@@ -394,6 +394,7 @@ int paged_kv_plan(const int *seq_lens, const int *new_lens, int n, int *block_ta
  *   k, v         [tokens, H_kv, d] rows, placed by their strides {token,
  *                head}; NULL = contiguous.
  *   d            64 or 128.
+ * k, v and the pools do not overlap.
  */
 int paged_kv_append(const void *k, const long long *k_strides, const void *v,
                     const long long *v_strides, void *k_cache, const long long *k_cache_strides,
@@ -432,7 +433,8 @@ size_t paged_attn_workspace_size(int n, int tokens, int H, int H_kv, int d);
  *   workspace    paged_attn_workspace_size bytes (up to 46 MB), 256-byte
  *                aligned, of any contents; calls that may run at the same
  *                time need one each.
- * Keys behind a row's last one do not reach it, whatever they hold.
+ * Keys behind a row's last one do not reach it, whatever they hold.  o, lse
+ * and workspace overlap nothing else.
  */
 int paged_attn_fwd(const void *q, const long long *q_strides, const void *k_cache,
                    const long long *k_cache_strides, const void *v_cache,

@@ -126,9 +126,9 @@ def paged_kv_plan(seq_lens, new_lens, block_table, free_list, counts, page_size:
     table, n, max_pages, stride = _table(block_table, dev)
     _first(free_list, "free_list", 1)
     pages = free_list.shape[0]
-    tokens = int(tokens)
-    if tokens < 0:
-        raise ValueError("tokens must not be negative")
+    tokens, page_size = int(tokens), int(page_size)
+    if not 0 <= tokens < 2 ** 31 or abs(page_size) >= 2 ** 31:
+        raise ValueError("tokens and page_size must be 32-bit integers, tokens not negative")
     own, given = [], (seq_lens_out, cu_q, slots, counts_out)
     shapes = ((n,), (n + 1,), (tokens,), (2,))
     out = tuple(torch.empty(shape, dtype=_I32, device=block_table.device) if t is None else t
@@ -139,7 +139,7 @@ def paged_kv_plan(seq_lens, new_lens, block_table, free_list, counts, page_size:
     _call(dev, stream, own, "paged_kv_plan", load_library().paged_kv_plan,
           _whole(seq_lens, "seq_lens", _I32, (n,), dev), _whole(new_lens, "new_lens", _I32, (n,), dev), n, table,
           stride, max_pages, _whole(free_list, "free_list", _I32, (pages,), dev), pages,
-          _whole(counts, "counts", _I32, (2,), dev), int(page_size), tokens,
+          _whole(counts, "counts", _I32, (2,), dev), page_size, tokens,
           _whole(seq_lens_out, "seq_lens_out", _I32, (n,), dev), _whole(cu_q, "cu_q", _I32, (n + 1,), dev),
           _whole(slots, "slots", _I32, (tokens,), dev), _whole(counts_out, "counts_out", _I32, (2,), dev))
     return out
@@ -218,6 +218,6 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_q, causal: boo
     _call(dev, stream, own, "paged_attn_fwd", lib.paged_attn_fwd, *q_at,
           *_elems(k_cache, "k_cache", dtype, pool, dev), *_elems(v_cache, "v_cache", dtype, pool, dev), table, stride,
           _whole(seq_lens, "seq_lens", _I32, (n,), dev), _whole(cu_q, "cu_q", _I32, (n + 1,), dev), *o_at, lse_at,
-          _DTYPES[dtype], n, T, H, H_kv, d, num_pages, page_size, max_pages, T if max_q is None else int(max_q),
+          _DTYPES[dtype], n, T, H, H_kv, d, num_pages, page_size, max_pages, T if max_q is None else min(T, int(max_q)),
           int(bool(causal)), 1.0 / math.sqrt(d) if scale is None else float(scale), ws_at, ws_bytes)
     return o, lse

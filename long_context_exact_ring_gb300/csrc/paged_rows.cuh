@@ -126,8 +126,8 @@ struct RowsParams {
 // leave the tcgen05 tile of 128 empty, and the products are not the bound.)
 // 64 ragged contexts up to 16K, 32 heads over 8, d 128: 330 us, 1.01 of measured
 // copy bandwidth; one context of 128K, 32 heads: 305 to 315 us, 1.02 to 1.05; 128 contexts of
-// 8K, 16 heads over 2, d 64: 0.94.  A lone short context (777 keys) takes 8 us,
-// a chain of latencies: lengths, page numbers, keys, merge.
+// 8K, 16 heads over 2, d 64: 0.94.  A lone short context (777 keys) takes 12 us,
+// launch included, a chain of latencies: lengths, page numbers, keys, merge.
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,

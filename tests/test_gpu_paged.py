@@ -79,6 +79,18 @@ def test_plan_over_odd_lengths_stays_inside(ra):
         guard[64:64 + tokens] = 55
 
 
+@pytest.mark.parametrize("tokens", [0, 5])
+def test_plan_without_requests(ra, tokens):
+    """A loop that has run dry: the pages stay free, no slot is given."""
+    free = _i32([4, 2, 0, 1, 3])
+    for in_place in (False, True):
+        counts, cu = _i32([3, 9]), _i32([77])
+        out = ra.paged_kv_plan(_i32([]), _i32([]), torch.empty(0, 4, dtype=torch.int32, device="cuda"), free, counts, 16,
+                               tokens, cu_q=cu, counts_out=counts if in_place else None)
+        assert [x.tolist() for x in out] == [[], [0], [-1] * tokens, [3, 0]]
+    assert free.tolist() == [4, 2, 0, 1, 3]
+
+
 # ---------------------------------------------------------------------------
 # Append
 # ---------------------------------------------------------------------------
@@ -169,7 +181,7 @@ def test_attn_not_causal(ra, batch, dtype, d):
     _check(ra, make(lens, news, 8, 4, d, 24, dtype, seed=3), causal=False, scale=0.3)
 
 
-@pytest.mark.parametrize("max_q", [1, 64, 10 ** 6])
+@pytest.mark.parametrize("max_q", [1, 64, 10 ** 6, 2 ** 32 + 1])
 def test_attn_does_not_depend_on_the_hint(ra, max_q):
     lens, news = BATCHES["chunks"]
     x = make(lens, news, 8, 2, 128, 16, torch.bfloat16, seed=9)

@@ -37,10 +37,6 @@ def test_plan_refuses(ra, change, code):
     assert _plan(ra, **change) == code
 
 
-def test_empty_plan_touches_nothing(ra):
-    assert _plan(ra, n=0, tokens=0, table=0, lens=0, slots=0) == 0
-
-
 def _strides(*x):
     return (ctypes.c_longlong * len(x))(*x)
 
