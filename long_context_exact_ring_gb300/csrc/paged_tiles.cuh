@@ -103,11 +103,12 @@ struct Walk {
     Request r;
     TileWork w;
     int req, kvh, t, k0, k1, total;
-    int turn, passed;        // see key_tile; key tiles of the pieces so far
+    int turn;                // see key_tile
+    unsigned passed;         // key tiles of the pieces so far
     long long left;          // cost of what follows this piece
 
     __device__ __forceinline__ Walk(const TileParams& p_, int req_, int kvh_, int t_, long long c0, long long share)
-        : p(p_), req(req_), kvh(kvh_), t(t_), passed(0), left(share)
+        : p(p_), req(req_), kvh(kvh_), t(t_), passed(0u), left(share)
     {
         load();
         cut(c0);
@@ -136,8 +137,8 @@ struct Walk {
         left -= c1 - c0;
         k0 = cut_units(c0, kExtra);
         k1 = cut_units(c1, kExtra);
-        turn = k1 - k0 == total ? passed % total : 0;
-        passed += k1 - k0;
+        turn = k1 - k0 == total ? (int)(passed % (unsigned)total) : 0;
+        passed += (unsigned)(k1 - k0);
     }
     // The j-th key tile of the piece: from the last to the first, so that the
     // blocks that take over a tile of the same keys, which all begin at its end,
