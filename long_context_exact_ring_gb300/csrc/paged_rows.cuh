@@ -38,6 +38,8 @@ struct Cfg {
 // contexts of up to 1153 keys, 32 heads of 64: 120, 88 and 76 us.
 constexpr int kExtra = 2;
 
+constexpr float kLeastBf16 = 9.18354962e-41f;    // 2^-133
+
 // A block's place in its share: units [u0, u1) of kUnit keys of a tile.
 template <int kUnit>
 struct Walk {
@@ -359,20 +361,27 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
 #pragma unroll
                     for (int y = 0; y < 4; ++y) st.acc[x][y] *= alpha[y >> 1];
             }
-            // Weights rounded to the operand type.  bf16's half step of 2^-8 would
-            // show in O, so what it leaves out is rounded and multiplied too, for 1 %
-            // of a long decode's time; fp16's half step of 2^-11 stays.  l sums the
-            // weights unrounded.
+            // Weights in the operand type.  fp16's half step of 2^-11 stays.  bf16's
+            // would show in O, so a weight is cut to its upper half and what that
+            // leaves is rounded and multiplied too, for 1 % of a long decode's time:
+            // 2^-16 of the weight is lost.  Cut, not rounded, and with the smallest
+            // bf16 in place of a rest of 0, both parts have the weight's sign: an
+            // infinity in V gives no NaN by the rest's 0 or -infinity.  l sums the
+            // weights as they are.
             uint32_t pa[kSteps16][4], pr[kSteps16][4];
 #pragma unroll
             for (int z = 0; z < kSteps16; ++z)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float w0 = s[2 * z + (i >> 1)][2 * (i & 1)], w1 = s[2 * z + (i >> 1)][2 * (i & 1) + 1];
-                    pa[z][i] = Op::pack(w0, w1);
-                    if constexpr (!kHalf)
-                        pr[z][i] = Op::pack(w0 - __uint_as_float(pa[z][i] << 16),
-                                            w1 - __uint_as_float(pa[z][i] & 0xffff0000u));
+                    if constexpr (kHalf) {
+                        pa[z][i] = Op::pack(w0, w1);
+                    } else {
+                        const uint32_t b0 = __float_as_uint(w0), b1 = __float_as_uint(w1);
+                        const float h0 = __uint_as_float(b0 & 0xffff0000u), h1 = __uint_as_float(b1 & 0xffff0000u);
+                        pa[z][i] = __byte_perm(b0, b1, 0x7632);
+                        pr[z][i] = Op::pack(fmaxf(w0 - h0, fminf(h0, kLeastBf16)), fmaxf(w1 - h1, fminf(h1, kLeastBf16)));
+                    }
                 }
 
             // ---- O += P V
