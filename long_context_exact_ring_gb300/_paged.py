@@ -9,7 +9,7 @@ import math
 
 import torch
 
-from ._binding import _check, load_library
+from ._binding import _check, _new, load_library
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 _LL2, _LL3 = ctypes.c_longlong * 2, ctypes.c_longlong * 3
@@ -89,18 +89,14 @@ def _pool_shape(k_cache):
     return tuple(k_cache.shape)
 
 
-def _call(device, stream, own, what, fn, *args):
-    """fn(*args, stream) with `device` current.  `own` are tensors made for
-    this call: on a stream that is not the one they were allocated on, their
-    memory must outlive the call there."""
+def _call(device, stream, what, fn, *args):
+    """fn(*args, stream) with `device` current."""
     if stream is None:
         handle = _current_stream(device)
     else:
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", device))
         handle = stream.cuda_stream
-        for t in own:
-            t.record_stream(stream)
     if _current_device() == device:
         rc = fn(*args, handle)
     else:
@@ -129,14 +125,11 @@ def paged_kv_plan(seq_lens, new_lens, block_table, free_list, counts, page_size:
     tokens, page_size = int(tokens), int(page_size)
     if not 0 <= tokens < 2 ** 31 or abs(page_size) >= 2 ** 31:
         raise ValueError("tokens and page_size must be 32-bit integers, tokens not negative")
-    own, given = [], (seq_lens_out, cu_q, slots, counts_out)
     shapes = ((n,), (n + 1,), (tokens,), (2,))
-    out = tuple(torch.empty(shape, dtype=_I32, device=block_table.device) if t is None else t
-                for t, shape in zip(given, shapes))
-    if stream is not None:
-        own = [t for t, g in zip(out, given) if g is None]
+    out = tuple(_new(stream, block_table, shape, _I32) if t is None else t
+                for t, shape in zip((seq_lens_out, cu_q, slots, counts_out), shapes))
     seq_lens_out, cu_q, slots, counts_out = out
-    _call(dev, stream, own, "paged_kv_plan", load_library().paged_kv_plan,
+    _call(dev, stream, "paged_kv_plan", load_library().paged_kv_plan,
           _whole(seq_lens, "seq_lens", _I32, (n,), dev), _whole(new_lens, "new_lens", _I32, (n,), dev), n, table,
           stride, max_pages, _whole(free_list, "free_list", _I32, (pages,), dev), pages,
           _whole(counts, "counts", _I32, (2,), dev), page_size, tokens,
@@ -157,7 +150,7 @@ def paged_kv_append(k, v, k_cache, v_cache, slots, *, stream=None):
     T, H_kv, d = shape
     num_pages, page_size = _pool_shape(k_cache)[:2]
     pool = (num_pages, page_size, H_kv, d)
-    _call(dev, stream, (), "paged_kv_append", load_library().paged_kv_append,
+    _call(dev, stream, "paged_kv_append", load_library().paged_kv_append,
           *_elems(k, "k", dtype, shape, dev), *_elems(v, "v", dtype, shape, dev),
           *_elems(k_cache, "k_cache", dtype, pool, dev), *_elems(v_cache, "v_cache", dtype, pool, dev),
           _whole(slots, "slots", _I32, (T,), dev), T, H_kv, d, num_pages, page_size)
@@ -193,29 +186,25 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_q, causal: boo
     table, n, max_pages, stride = _table(block_table, dev)
     lib = load_library()
     # what is made here needs no check
-    own = []
     q_at = _elems(q, "q", dtype, shape, dev)
     if o is None:
-        o = torch.empty_like(q)
-        own.append(o)
+        o = _new(stream, q)
         o_at = (o.data_ptr(), q_at[1] and _LL2(o.stride(0), o.stride(1)))
     else:
         o_at = _elems(o, "o", dtype, shape, dev)
     if lse is None:
-        lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-        own.append(lse)
+        lse = _new(stream, q, (H, T), torch.float32)
         lse_at = lse.data_ptr()
     else:
         lse_at = _whole(lse, "lse", torch.float32, (H, T), dev)
     if workspace is None:
         ws_bytes = paged_attn_workspace_size(n, T, H, H_kv, d)
-        workspace = torch.empty(max(ws_bytes, 1), dtype=torch.uint8, device=q.device)
-        own.append(workspace)
+        workspace = _new(stream, q, (max(ws_bytes, 1),), torch.uint8)
         ws_at = workspace.data_ptr()
     else:
         ws_at = _whole(workspace, "workspace", torch.uint8, getattr(workspace, "shape", None), dev)
         ws_bytes = workspace.numel()
-    _call(dev, stream, own, "paged_attn_fwd", lib.paged_attn_fwd, *q_at,
+    _call(dev, stream, "paged_attn_fwd", lib.paged_attn_fwd, *q_at,
           *_elems(k_cache, "k_cache", dtype, pool, dev), *_elems(v_cache, "v_cache", dtype, pool, dev), table, stride,
           _whole(seq_lens, "seq_lens", _I32, (n,), dev), _whole(cu_q, "cu_q", _I32, (n + 1,), dev), *o_at, lse_at,
           _DTYPES[dtype], n, T, H, H_kv, d, num_pages, page_size, max_pages, T if max_q is None else min(T, int(max_q)),

@@ -1,0 +1,70 @@
+"""Calls on a stream of their own (stream=): what they allocate is not memory
+that work queued on the current stream still uses, and what they return may be
+used on the current stream and dropped there."""
+import pytest
+import torch
+
+from _paged import make
+
+pytestmark = pytest.mark.gpu
+
+SLEEP = 100_000_000     # clock ticks, about 50 ms
+
+
+@pytest.fixture(scope="module")
+def ra():
+    import long_context_exact_ring_gb300 as m
+    from long_context_exact_ring_gb300 import build
+    build.build()
+    return m
+
+
+def _free_memory_with_queued_writes(sizes):
+    """Blocks of these sizes, free to the current stream, which has yet to
+    write them."""
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    blocks = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in sizes]
+    torch.cuda._sleep(SLEEP)
+    for b in blocks:
+        b.fill_(0x7f)
+
+
+def _check(call, sizes):
+    """call(stream) -> tensors; the same results whatever the current stream is at."""
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    _free_memory_with_queued_writes(sizes)
+    got = call(side)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # read late on the current stream, dropped, and the call repeated
+    torch.cuda._sleep(SLEEP)
+    kept = [t.clone() for t in got]
+    del got
+    for _ in range(2):
+        for t in call(side):
+            with torch.cuda.stream(side):
+                t.zero_()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(kept, want))
+
+
+@pytest.mark.parametrize("news", [[1, 1, 1], [1, 130, 30]])
+def test_paged_attn_on_its_own_stream(ra, news):
+    x = make([5000, 2000, 77], news, 8, 2, 128, 16, torch.bfloat16, seed=12)
+    args = [x[n].cuda() for n in ("q", "k_cache", "v_cache", "table", "seq_lens", "cu_q")]
+    T, H, d = args[0].shape
+    _check(lambda s: ra.paged_attn_fwd(*args, True, stream=s),
+           [2 * T * H * d, 4 * T * H, ra.paged_attn_workspace_size(3, T, H, 2, d)])
+
+
+def test_paged_plan_on_its_own_stream(ra):
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n, tokens = 300, 5000
+    lens, new = torch.arange(n, **i32), torch.full((n,), 16, **i32)
+    table = torch.arange(n * 40, **i32).reshape(n, 40)
+    free, counts = torch.arange(n * 40, n * 42, **i32), torch.tensor([n * 2, 0], **i32)
+    _check(lambda s: ra.paged_kv_plan(lens, new, table, free, counts, 16, tokens, stream=s),
+           [4 * n, 4 * (n + 1), 4 * tokens, 8])
