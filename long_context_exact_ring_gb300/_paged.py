@@ -1,6 +1,8 @@
 """Binding of the paged key/value cache calls: argument marshalling only, as
 in _binding.py, for tensors of any device (the call runs on the device of its
-tensors, on that device's current stream unless ``stream`` names one)."""
+tensors, on that device's current stream unless ``stream``, a torch stream or a
+handle, names one: the caller orders it behind what writes the inputs, and what
+reads the results behind it)."""
 from __future__ import annotations
 
 import ctypes
@@ -94,9 +96,7 @@ def _call(device, stream, what, fn, *args):
     if stream is None:
         handle = _current_stream(device)
     else:
-        if not isinstance(stream, torch.cuda.Stream):
-            stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", device))
-        handle = stream.cuda_stream
+        handle = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
     if _current_device() == device:
         rc = fn(*args, handle)
     else:

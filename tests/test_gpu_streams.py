@@ -68,3 +68,28 @@ def test_paged_plan_on_its_own_stream(ra):
     free, counts = torch.arange(n * 40, n * 42, **i32), torch.tensor([n * 2, 0], **i32)
     _check(lambda s: ra.paged_kv_plan(lens, new, table, free, counts, 16, tokens, stream=s),
            [4 * n, 4 * (n + 1), 4 * tokens, 8])
+
+
+@pytest.mark.parametrize("handle", [0, 1, 2, "of a stream"])
+def test_paged_calls_on_a_stream_given_by_its_handle(ra, handle):
+    """The calls run on the stream that the handle names (0 to 2: the default
+    ones), behind what is queued there."""
+    x = make([700, 90], [1, 30], 8, 2, 128, 16, torch.bfloat16, seed=3)
+    q, k, v, table, lens, cu = (x[n].cuda() for n in ("q", "k_cache", "v_cache", "table", "seq_lens", "cu_q"))
+    want = ra.paged_attn_fwd(q, k, v, table, lens, cu, True)
+    stream = torch.cuda.Stream() if handle == "of a stream" else torch.cuda.default_stream()
+    late, rows, pools = torch.zeros_like(q), k[:2, 0], [torch.zeros_like(k) for _ in range(2)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(SLEEP)
+        late.copy_(q)
+        for p in pools:
+            p.fill_(1.0)
+    handle = stream.cuda_stream if handle == "of a stream" else handle
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = ra.paged_attn_fwd(late, k, v, table, lens, cu, True, stream=handle)
+        ra.paged_kv_append(rows, rows, *pools, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), stream=handle)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for p in pools:
+        assert torch.equal(p[0, :2].nan_to_num(7.0), rows.nan_to_num(7.0)) and (p[1:] == 1).all()
