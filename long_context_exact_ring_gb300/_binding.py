@@ -250,9 +250,9 @@ def ring_attn_fwd(q, k, v, P: int, causal: bool, scale: float | None = None, *,
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     if o is None:
-        o = torch.empty_like(q)
+        o = _new(stream, q)
     if lse is None:
-        lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device)
+        lse = _new(stream, q, (B, H, S), torch.float32)
     _need(o, "o", torch.bfloat16, q.shape, rows_ok=True)
     _need(lse, "lse", torch.float32, (B, H, S))
     lib = load_library()
@@ -293,13 +293,13 @@ def ring_attn_fwd_f32(q, k, v, P: int, causal: bool, scale: float | None = None,
     _need(v, "v", torch.float32, (B, H_kv, S, d))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None else lse
+    o = _new(stream, q) if o is None else o
+    lse = _new(stream, q, (B, H, S), torch.float32) if lse is None else lse
     _need(o, "o", torch.float32, q.shape)
     _need(lse, "lse", torch.float32, (B, H, S))
     need = fwd_f32_workspace_size(B, H, H_kv, S, d)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, q, (max(need, 1),), torch.uint8)
     _need(workspace, "workspace", torch.uint8)
     rc = load_library().ring_attn_fwd_f32(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(),
                                           lse.data_ptr(), B, H, H_kv, S, d, int(P),
@@ -327,13 +327,13 @@ def ring_attn_fwd_ulysses_emulated(q, k, v, P: int, causal: bool, scale: float |
         _need(t, n, torch.bfloat16)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None else lse
+    o = _new(stream, q) if o is None else o
+    lse = _new(stream, q, (B, H, S), torch.float32) if lse is None else lse
     _need(o, "o", torch.bfloat16, q.shape)
     _need(lse, "lse", torch.float32, (B, H, S))
     need = ulysses_workspace_size(B, H, H_kv, S, d)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, q, (max(need, 1),), torch.uint8)
     _need(workspace, "workspace", torch.uint8)
     rc = load_library().ring_attn_fwd_ulysses_emulated(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, H, H_kv, S, d,
@@ -360,13 +360,13 @@ def ring_attn_fwd_emulated(q, k, v, P: int, causal: bool, scale: float | None = 
     _need(v, "v", torch.bfloat16, q.shape)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    o = torch.empty_like(q) if o is None else o
-    lse = torch.empty((B, H, S), dtype=torch.float32, device=q.device) if lse is None else lse
+    o = _new(stream, q) if o is None else o
+    lse = _new(stream, q, (B, H, S), torch.float32) if lse is None else lse
     _need(o, "o", torch.bfloat16, q.shape)
     _need(lse, "lse", torch.float32, (B, H, S))
     need = emulated_workspace_size(B, H, S, d)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, q, (max(need, 1),), torch.uint8)
     _need(workspace, "workspace", torch.uint8)
     rc = load_library().ring_attn_fwd_emulated(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                                o.data_ptr(), lse.data_ptr(), B, H, S, d, int(P),
@@ -395,15 +395,15 @@ def ring_attn_bwd(q, k, v, o, lse, dO, P: int, causal: bool, scale: float | None
     _need(lse, "lse", torch.float32, (B, H, S))
     if scale is None:
         scale = 1.0 / math.sqrt(d)
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    dq = _new(stream, q) if dq is None else dq
+    dk = _new(stream, k) if dk is None else dk
+    dv = _new(stream, v) if dv is None else dv
     _need(dq, "dq", torch.bfloat16, q.shape, rows_ok=True)
     _need(dk, "dk", torch.bfloat16, k.shape, rows_ok=True)
     _need(dv, "dv", torch.bfloat16, v.shape, rows_ok=True)
     need = bwd_workspace_size(B, H, S, d)
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=q.device)
+        workspace = _new(stream, q, (max(need, 1),), torch.uint8)
     _need(workspace, "workspace", torch.uint8)
     lib = load_library()
     if not _all_contiguous(q, k, v, o, dO, dq, dk, dv):
@@ -466,8 +466,8 @@ def attn_merge_partials(o_a, lse_a, o_b, lse_b, *, o_out=None, lse_out=None, str
     _need(o_b, "o_b", torch.float32, o_a.shape)
     _need(lse_a, "lse_a", torch.float32, (B, H, S))
     _need(lse_b, "lse_b", torch.float32, (B, H, S))
-    o_out = torch.empty_like(o_a) if o_out is None else o_out
-    lse_out = torch.empty_like(lse_a) if lse_out is None else lse_out
+    o_out = _new(stream, o_a) if o_out is None else o_out
+    lse_out = _new(stream, lse_a) if lse_out is None else lse_out
     _need(o_out, "o_out", torch.float32, o_a.shape)
     _need(lse_out, "lse_out", torch.float32, (B, H, S))
     rc = load_library().attn_merge_partials(o_a.data_ptr(), lse_a.data_ptr(), o_b.data_ptr(),

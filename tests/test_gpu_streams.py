@@ -93,3 +93,28 @@ def test_paged_calls_on_a_stream_given_by_its_handle(ra, handle):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     for p in pools:
         assert torch.equal(p[0, :2].nan_to_num(7.0), rows.nan_to_num(7.0)) and (p[1:] == 1).all()
+
+
+def _ring_inputs(dtype=torch.bfloat16):
+    g = torch.Generator("cuda").manual_seed(4)
+    return [torch.randn((1, 4, 512, 64), generator=g, device="cuda").to(dtype) for _ in range(4)]
+
+
+@pytest.mark.parametrize("name", ["ring_attn_fwd", "ring_attn_fwd_f32", "ring_attn_fwd_emulated",
+                                  "ring_attn_fwd_ulysses_emulated"])
+def test_ring_forward_on_its_own_stream(ra, name):
+    q, k, v, _ = _ring_inputs(torch.float32 if name == "ring_attn_fwd_f32" else torch.bfloat16)
+    work = {"ring_attn_fwd": 1, "ring_attn_fwd_f32": ra.fwd_f32_workspace_size(1, 4, 4, 512, 64),
+            "ring_attn_fwd_emulated": ra.emulated_workspace_size(1, 4, 512, 64),
+            "ring_attn_fwd_ulysses_emulated": ra.ulysses_workspace_size(1, 4, 4, 512, 64)}[name]
+    _check(lambda s: getattr(ra, name)(q, k, v, 2, True, stream=s), [q.numel() * q.element_size(), 4 * 4 * 512, work])
+
+
+def test_ring_backward_and_merge_on_their_own_stream(ra):
+    q, k, v, do = _ring_inputs()
+    o, lse = ra.ring_attn_fwd(q, k, v, 2, True)
+    # dQ is summed in no fixed order: dK and dV are compared bit by bit
+    _check(lambda s: ra.ring_attn_bwd(q, k, v, o, lse, do, 2, True, stream=s)[1:],
+           [2 * q.numel()] * 3 + [ra.bwd_workspace_size(1, 4, 512, 64)])
+    a, b, lse_b = o.float(), do.float(), lse + 1
+    _check(lambda s: ra.attn_merge_partials(a, lse, b, lse_b, stream=s), [4 * q.numel(), 4 * 4 * 512])
