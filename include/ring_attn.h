@@ -379,7 +379,8 @@ typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
  * seq_lens_out may be seq_lens and counts_out may be counts (a loop's state,
  * updated in place); otherwise buffers do not overlap.  Where they are not
  * updated in place the call can be repeated with the same result.
- * n * max_pages, num_pages and max_pages * page_size are at most 2^30.
+ * n * max_pages, num_pages, tokens and max_pages * page_size are at most 2^30
+ * (more: RA_ERR_UNSUPPORTED).
  */
 int paged_kv_plan(const int *seq_lens, const int *new_lens, int n, int *block_table,
                   long long table_stride, int max_pages, int *free_list, int num_pages,

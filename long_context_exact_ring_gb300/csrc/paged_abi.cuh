@@ -238,7 +238,7 @@ int paged_kv_plan(const int* seq_lens, const int* new_lens, int n, int* block_ta
     if (rc != RA_OK) return rc;
     if (max_pages < 1 || table_stride < max_pages) return RA_ERR_INVALID_ARG;
     if (n > ra::paged::kMaxRequests || (long long)n * max_pages > (1ll << 30) || num_pages > (1 << 30) ||
-        (long long)max_pages * page_size > (1ll << 30))
+        tokens > (1 << 30) || (long long)max_pages * page_size > (1ll << 30))
         return RA_ERR_UNSUPPORTED;
     if (!free_list || !counts || !counts_out || !cu_q || (tokens > 0 && !slots) ||
         (n > 0 && (!seq_lens || !new_lens || !block_table || !seq_lens_out)))
