@@ -4,7 +4,7 @@
 #pragma once
 
 #include "paged_index.h"
-#include "sm103_ptx.cuh"
+#include "paged_ptx.cuh"
 
 namespace ra {
 namespace paged {

@@ -20,7 +20,6 @@ namespace ra {
 enum : uint32_t {
     kStatusTimeout = 1u,   // a bounded wait ran out
     kStatusAborted = 2u,   // a CTA left early because another role timed out
-    kStatusBadPage = 4u,   // a page or slot outside its pool was met and not followed
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p)
@@ -132,24 +131,6 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
 {
     if (mbar_try_wait(bar, parity)) return true;
     return mbar_wait_slow(bar, parity, w);
-}
-
-// mbar_wait without a call: a kernel that moves registers between its warps
-// (setmaxnreg) may call no function.
-__device__ __forceinline__ bool mbar_wait_inline(uint32_t bar, uint32_t parity, const WaitCtl& w)
-{
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
-#pragma unroll 1
-    while (true) {
-        if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
-        if (*w.abort_flag) return false;
-        if (globaltimer_ns() - t0 > w.limit_ns) {
-            *w.abort_flag = 1;
-            atomicOr(w.status, kStatusTimeout);
-            return false;
-        }
-    }
 }
 
 // Non-blocking test of a phase.
