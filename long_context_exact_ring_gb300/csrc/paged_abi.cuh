@@ -84,18 +84,49 @@ cudaError_t configure_attn_kernels()
     return e;
 }
 
-// Shared-memory and cluster limits of the kernels, once per device.
-cudaError_t configure_paged_kernels()
+cudaError_t configure_plan_kernel()
 {
     cudaError_t e = cudaFuncSetAttribute(ra::paged::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)ra::paged::plan_smem(ra::paged::kMaxRequests));
     if (e == cudaSuccess)
         e = cudaFuncSetAttribute(ra::paged::paged_plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e == cudaSuccess) e = configure_attn_kernels<64, false>();
+    return e;
+}
+
+cudaError_t configure_all_attn_kernels()
+{
+    cudaError_t e = configure_attn_kernels<64, false>();
     if (e == cudaSuccess) e = configure_attn_kernels<64, true>();
     if (e == cudaSuccess) e = configure_attn_kernels<128, false>();
     if (e == cudaSuccess) e = configure_attn_kernels<128, true>();
     return e;
+}
+
+// Kernels that have to be configured before their first launch on a device.
+// No call depends on kernels that it does not launch.
+struct Configured {
+    cudaError_t (*configure)();
+    const char* what;
+    std::atomic<bool> ready[kMaxDevices];
+};
+Configured g_plan_kernel{configure_plan_kernel, "paged_plan_kernel set-up", {}};
+Configured g_attn_kernels{configure_all_attn_kernels, "paged attention kernels' set-up", {}};
+
+// device_state, and those kernels configured.
+int configured_state(DeviceState** out, Configured& kernels)
+{
+    const int rc = device_state(out);
+    if (rc != RA_OK) return rc;
+    std::atomic<bool>& ready = kernels.ready[*out - g_dev];
+    if (ready.load(std::memory_order_acquire)) return RA_OK;
+    std::lock_guard<std::mutex> lock(g_mu);
+    if (!ready.load(std::memory_order_relaxed)) {
+        CaptureRelaxed relaxed;      // as in device_state
+        const cudaError_t e = kernels.configure();
+        if (e != cudaSuccess) return fail_cuda(e, kernels.what);
+        ready.store(true, std::memory_order_release);
+    }
+    return RA_OK;
 }
 
 // 4-D tiled map of 2-byte elements with 128-byte swizzle, 64 columns wide.  L2
@@ -247,7 +278,7 @@ int paged_kv_plan(const int* seq_lens, const int* new_lens, int n, int* block_ta
     for (const void* x : all)
         if (!aligned4(x)) return RA_ERR_INVALID_ARG;
     DeviceState* st = nullptr;
-    int e = device_state(&st);
+    const int e = configured_state(&st, g_plan_kernel);
     if (e != RA_OK) return e;
     ra::paged::PlanParams p{seq_lens,     new_lens, block_table, table_stride, free_list, counts, seq_lens_out,
                             cu_q,         slots,    counts_out,  n,            max_pages, num_pages, page_size,
@@ -349,7 +380,7 @@ int paged_attn_fwd(const void* q, const long long* q_strides, const void* k_cach
         workspace_bytes < paged_attn_workspace_size(n, tokens, H, H_kv, d))
         return RA_ERR_INVALID_ARG;
     DeviceState* st = nullptr;
-    if ((rc = device_state(&st)) != RA_OK) return rc;
+    if ((rc = configured_state(&st, g_attn_kernels)) != RA_OK) return rc;
 
     ra::paged::AttnParams p;
     p.q = static_cast<const uint16_t*>(q);

@@ -50,8 +50,6 @@ int fail_cuda(cudaError_t e, const char* what)
     return RA_ERR_CUDA;
 }
 
-cudaError_t configure_paged_kernels();   // paged_abi.cuh
-
 // While it lives, this thread may make calls that a stream capture forbids
 // by default; none of the set-up's touches a stream.
 struct CaptureRelaxed {
@@ -101,7 +99,6 @@ int device_state(DeviceState** out)
                                      cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      ra::fwd::Cfg<128>::kSmemBytes);
         if (e == cudaSuccess) e = ra::bwd::configure_kernels();
-        if (e == cudaSuccess) e = configure_paged_kernels();
         if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute");
         st.ready = true;
     }
