@@ -343,10 +343,13 @@ int attn_merge_partials(const float *o_a, const float *lse_a, const float *o_b, 
  * Elements are bf16 (RA_BF16) or fp16 (RA_FP16).
  *
  * What these calls read on the device cannot be checked on the host.  A page
- * or slot outside the pool is never followed: its keys read as rows of
- * zeros, its tokens are not appended, and ring_attn_check_status then
- * reports RA_ERR_BAD_PAGE.  Lengths are cut to what the tables and buffers
- * hold.
+ * or slot outside the pool is never followed: paged_attn_fwd reads its keys
+ * as rows of zeros, paged_kv_append leaves its token out, and
+ * ring_attn_check_status then reports RA_ERR_BAD_PAGE.  paged_kv_plan itself
+ * reports none: its tokens on such a page get the slot -1, which
+ * paged_kv_append takes for no slot, and the request grows; the step's
+ * paged_attn_fwd reads the page and reports it.  Lengths are cut to what the
+ * tables and buffers hold.
  * ------------------------------------------------------------------------ */
 typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
 
