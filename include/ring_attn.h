@@ -379,6 +379,13 @@ typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
  * granted keeps its length, its pages and its tokens' places in cu_q; try it
  * again when there are pages.  (Its rows of paged_attn_fwd in this step are
  * those of the last tokens that its cache holds: discard them.)
+ * Tables, lengths and counts are the loop's state, and a request's pages are
+ * known by its length alone: whoever shortens a request, to take back those
+ * tokens of a draft that were not accepted, puts the pages behind the new
+ * length, entries ceil(new / page_size) .. ceil(old / page_size) - 1 of its
+ * row, on the stack and raises counts[0] by their number.  The next step
+ * would take new pages in their place, and they would be lost.  A page stands
+ * in one request's row at a time: one in two rows would be given back twice.
  * seq_lens_out may be seq_lens and counts_out may be counts (a loop's state,
  * updated in place); otherwise buffers do not overlap.  Where they are not
  * updated in place the call can be repeated with the same result.
