@@ -118,3 +118,29 @@ def test_ring_backward_and_merge_on_their_own_stream(ra):
            [2 * q.numel()] * 3 + [ra.bwd_workspace_size(1, 4, 512, 64)])
     a, b, lse_b = o.float(), do.float(), lse + 1
     _check(lambda s: ra.attn_merge_partials(a, lse, b, lse_b, stream=s), [4 * q.numel(), 4 * 4 * 512])
+
+
+@pytest.mark.parametrize("fork", [False, True])
+def test_captured_on_a_stream_that_is_named(ra, fork):
+    """stream= inside a capture: the capture's own stream, or one that forks off
+    it and joins it again."""
+    x = make([700, 90, 3000], [1, 30, 1], 8, 2, 128, 16, torch.bfloat16, seed=3)
+    args = [x[n].cuda() for n in ("q", "k_cache", "v_cache", "table", "seq_lens", "cu_q")]
+    want = ra.paged_attn_fwd(*args, True)
+    q, k, v, _ = _ring_inputs()
+    want_ring = ra.ring_attn_fwd(q, k, v, 2, True)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        stream = side if fork else main
+        side.wait_stream(main)
+        got = ra.paged_attn_fwd(*args, True, stream=stream)
+        ring = ra.ring_attn_fwd(q, k, v, 2, True, stream=stream)
+        main.wait_stream(side)
+    for _ in range(2):
+        for t in (*got, *ring):
+            t.fill_(3.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*got, *ring), (*want, *want_ring)))
