@@ -34,8 +34,8 @@ struct Cfg {
 
 // What a tile costs beside its keys, in units: the states of eight warps are
 // merged and the results written, 2 to 3 us against 1.5 us for a unit.  64
-// ragged contexts up to 16K: 342 us without it, 333 with 1, 329 with 2; 64
-// contexts of up to 1153 keys, 32 heads of 64: 120, 88 and 76 us.
+// ragged contexts up to 16K, on one box in turn: 342 us without it, 333 with 1,
+// 329 with 2; 64 contexts of up to 1153 keys, 32 heads of 64: 120, 88 and 76 us.
 constexpr int kExtra = 2;
 
 constexpr float kLeastBf16 = 9.18354962e-41f;    // 2^-133
@@ -126,10 +126,11 @@ struct RowsParams {
 //
 // Bound by HBM: K and V are read once per 16 packed rows.  (mma.sync: 16 rows
 // leave the tcgen05 tile of 128 empty, and the products are not the bound.)
-// 64 ragged contexts up to 16K, 32 heads over 8, d 128: 330 us, 1.01 of measured
-// copy bandwidth; one context of 128K, 32 heads: 305 to 315 us, 1.02 to 1.05; 128 contexts of
-// 8K, 16 heads over 2, d 64: 0.94.  A lone short context (777 keys) takes 12 us,
-// launch included, a chain of latencies: lengths, page numbers, keys, merge.
+// 64 ragged contexts up to 16K, 32 heads over 8, d 128: 335 to 345 us, 0.97 to 1.00
+// of measured copy bandwidth; one context of 128K, 32 heads: 310 to 320 us, 1.00
+// to 1.03; 128 contexts of 8K, 16 heads over 2, d 64: 91 us, 0.88.  A lone short
+// context (777 keys) takes 12 us, launch included, a chain of latencies: lengths,
+// page numbers, keys, merge.
 template <int D, bool kHalf>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
@@ -366,8 +367,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_consta
             // leaves is rounded and multiplied too, for 1 % of a long decode's time:
             // 2^-16 of the weight is lost.  Cut, not rounded, and with the smallest
             // bf16 in place of a rest of 0, both parts have the weight's sign: an
-            // infinity in V gives no NaN by the rest's 0 or -infinity.  l sums the
-            // weights as they are.
+            // infinity in V gives no NaN by the rest's 0 or -infinity.  (Against a
+            // rounded upper half: long decodes the same, 64 contexts of up to 1153
+            // keys, d 64, 77.7 -> 79.2 us.)  l sums the weights as they are.
             uint32_t pa[kSteps16][4], pr[kSteps16][4];
 #pragma unroll
             for (int z = 0; z < kSteps16; ++z)

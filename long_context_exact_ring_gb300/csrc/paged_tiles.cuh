@@ -27,9 +27,13 @@
 //
 // Bound, at d 128, by the softmax and its tile's two products taking turns (of
 // 2650 cycles a key tile, 1400 and 1250; the tensor core is at work for 2050 of
-// them), at d 64 by the softmax warps' instructions.  2048 tokens at the end of
-// 64K, 32 heads over 8: 1.53 us a key tile, 1670 TFLOP/s (0.85 of measured) at d
-// 128, 1.30 us at d 64.  Short pieces cost 5 to 6 us beside their keys (kExtra).
+// them), at d 64 by latency: an instruction in 46 % of the cycles, exponentials
+// 40 %, tensor cores 39 %; in the other cycles no warp is ready, as two softmax
+// warps to a scheduler do not hide their own chains.  2048 tokens at the end of
+// 64K, 32 heads over 8: 1.53 us a key tile, 1670 TFLOP/s (0.86 of measured) at d
+// 128, 1.30 us at d 64, calls apart.  Back to back, when power lowers the clock,
+// 2048 over 128K run at 1540 TFLOP/s.  Short pieces cost 5 to 6 us beside their
+// keys (kExtra).
 // Blocks of one key/value head read its keys at the same time, from L2 (see
 // Walk::key_tile).
 #pragma once
@@ -145,7 +149,7 @@ struct Walk {
     // read them at the same time, and those that leave one to the next block,
     // which all end at its beginning, too.  A whole tile between the two goes
     // round from where the pieces before it got to.  L2 then serves what HBM had
-    // to: 2048 tokens over 128K 2936 us in ascending order, 2846 descending,
+    // to: 2048 tokens over 128K, calls apart, 2936 us in ascending order, 2846 descending,
     // 2624 with whole tiles turned.
     __device__ __forceinline__ int key_tile(int j) const
     {
