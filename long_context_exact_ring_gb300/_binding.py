@@ -179,20 +179,20 @@ def _stream(stream) -> int:
 def _new(stream, like, shape=None, dtype=None):
     """Memory for a call on ``stream``: a tensor like `like`, or of a shape and
     type on its device, from that stream's own memory.  The current stream's
-    (``stream`` None) may still be in use by what is queued there, which
-    orders nothing on another stream.  The caller may use it on the current
-    stream too."""
-    if stream is None:
-        return torch.empty_like(like) if shape is None else torch.empty(shape, dtype=dtype, device=like.device)
-    if not isinstance(stream, torch.cuda.Stream):
-        # 0, 1 and 2 name the default streams, which order one another's work
-        handle = int(stream)
-        stream = (torch.cuda.ExternalStream(handle, device=like.device) if handle > 2
-                  else torch.cuda.default_stream(like.device))
-    with torch.cuda.stream(stream):
-        t = _new(None, like, shape, dtype)
-    t.record_stream(torch.cuda.current_stream(like.device))
-    return t
+    may still be in use by what is queued there, which orders nothing on
+    another stream.  The caller may use it on the current stream too."""
+    if stream is not None:
+        handle, current = _stream(stream), torch.cuda.current_stream(like.device)
+        if handle != current.cuda_stream:
+            if not isinstance(stream, torch.cuda.Stream):
+                # 0, 1 and 2 name the default streams, which order one another's work
+                stream = (torch.cuda.ExternalStream(handle, device=like.device) if handle > 2
+                          else torch.cuda.default_stream(like.device))
+            with torch.cuda.stream(stream):
+                t = _new(None, like, shape, dtype)
+            t.record_stream(current)
+            return t
+    return torch.empty_like(like) if shape is None else torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _need(t: torch.Tensor, name: str, dtype, shape=None, rows_ok: bool = False):
