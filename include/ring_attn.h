@@ -469,9 +469,9 @@ int ring_attn_schedule(int P, int causal, int i, int *out_j, int *out_kind, int 
 /*
  * Synchronizes `stream`, then reads and clears the current device's status
  * word.  RA_OK if no kernel reported a problem since the last check,
- * RA_ERR_DEVICE_TIMEOUT if a bounded wait ran out, RA_ERR_BAD_PAGE if a
- * paged call met a page or slot outside its pool, RA_ERR_CUDA if the
- * stream reported an error.
+ * RA_ERR_DEVICE_TIMEOUT if a bounded wait ran out, RA_ERR_BAD_PAGE if
+ * paged_attn_fwd met a page or paged_kv_append a slot outside its pool,
+ * RA_ERR_CUDA if the stream reported an error.
  */
 int ring_attn_check_status(void *stream);
 
