@@ -599,8 +599,11 @@ int paged_kv_append_rope(const void *q, const long long *q_strides, const void *
  *   drop         [n] int32 drafted tokens that do not stand: paged_kv_trim's.
  * A request without rows gets 0, -1 and 0.  A token outside the vocabulary
  * does not stand.  Probabilities that are NaN or below 0 count as 0 in w, those
- * above 1 as 1; w is summed exactly, in whole units of 2^-44, so the same
- * inputs give the same tokens, whatever else runs.
+ * above 1 as 1.  Weights are held in whole units, cut: of 2^-44 or, where their
+ * sum is below 2^-8, of at most 2^-36 of the sum or of 2^-149, the differences
+ * rounded to fp32 first.  So at most vocab * 2^-36 of the sum is lost, however
+ * small it is, and only rows that are 0 count as 0 throughout; units are summed
+ * exactly, so the same inputs give the same tokens, whatever else runs.
  * vocab up to 2^18, n up to 2^20 (else RA_ERR_UNSUPPORTED).  Outputs overlap
  * nothing.
  * ------------------------------------------------------------------------ */

@@ -38,8 +38,9 @@ struct Params {
 // A probability in units of 2^-44, cut to whole ones: 2^22 upper + lower, each
 // part kOffset too large.  What is no number or below 0 is 0, what is above 1
 // is 1.  Sums of up to 2^18 of them are exact in 64 bits, so they do not depend
-// on how the row is shared out, and the token drawn is the same in any order;
-// 2^-44 of a probability is less than the rounding of any above 2^-20.
+// on how the row is shared out, and the token drawn is the same in any order.
+// What is cut off counts against the sum that is drawn from: where that is below
+// kLeast units the weights are taken again in finer ones (see draw).
 //
 // An addition of 2, rounded down, leaves 22 bits behind the point in a float's
 // last bits.  (Conversions to 64-bit integers run at one or two a cycle and SM:
@@ -91,91 +92,122 @@ __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.w
 // What the token behind is drawn from.
 enum class Weights { kTarget, kRest, kOthers };     // a row, max(target - draft, 0), a row without one token
 
-// Weight of token x.
-template <Weights kWhat>
-__device__ __forceinline__ unsigned long long weight_of(const float* target, const float* draft, int gone, int x)
+// A weight in units of 2^-44, or, kFiner, of 2^-44 / scale, from a target's and a
+// draft's probability.  kFiner, a difference is taken in fp32 first, off by 2^-24 of
+// itself, and is 0 only where it is none; a power of two as scale rounds nothing.
+template <Weights kWhat, bool kFiner>
+__device__ __forceinline__ unsigned long long weight(float target, float draft, float scale)
 {
-    const Fixed f(target[x]);
-    if constexpr (kWhat == Weights::kRest) return above(f, Fixed(draft[x]));
-    else return kWhat == Weights::kOthers && x == gone ? 0ull : f.value();
+    if constexpr (kFiner) {
+        float w = __saturatef(target);
+        if constexpr (kWhat == Weights::kRest) w = w - __saturatef(draft);
+        return Fixed(w * scale).value();
+    } else if constexpr (kWhat == Weights::kRest) {
+        return above(Fixed(target), Fixed(draft));
+    } else {
+        return Fixed(target).value();
+    }
 }
 
-// Sum of the weights of tokens x, x + step, ... below x1.  The loads of kAhead
-// tokens are in flight together.
-template <Weights kWhat>
-__device__ __forceinline__ unsigned long long sum_weights(const float* target, const float* draft, int gone, int x,
-                                                          int x1, int step)
-{
-    constexpr int kAhead = 16;
-    unsigned long long sum = 0;
-    for (; x + (kAhead - 1) * step < x1; x += kAhead * step) {
-        float f[kAhead], g[kAhead];
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            f[e] = target[x + e * step];
-            if constexpr (kWhat == Weights::kRest) g[e] = draft[x + e * step];
-        }
-#pragma unroll
-        for (int e = 0; e < kAhead; ++e) {
-            if constexpr (kWhat == Weights::kRest) sum += above(Fixed(f[e]), Fixed(g[e]));
-            else sum += kWhat == Weights::kOthers && x + e * step == gone ? 0ull : Fixed(f[e]).value();
-        }
+// A row's weights: of a request's target and, for kRest, its draft; kOthers,
+// token `gone` has none.
+template <Weights kWhat, bool kFiner>
+struct Row {
+    const float* target;
+    const float* draft;
+    int gone;
+    float scale;
+    __device__ __forceinline__ unsigned long long at(int x) const
+    {
+        if (kWhat == Weights::kOthers && x == gone) return 0ull;
+        return weight<kWhat, kFiner>(target[x], kWhat == Weights::kRest ? draft[x] : 0.f, scale);
     }
-    for (; x < x1; x += step) sum += weight_of<kWhat>(target, draft, gone, x);
-    return sum;
-}
+    // Sum of the weights of tokens x, x + step, ... below x1, kAhead of them loaded
+    // in front of their sums: all at once from one row; from two, whose values would
+    // take all of the 32 registers, the compiler holds fewer.  (64 requests over
+    // 131071 tokens, two rows, 18.4 us, 18.8 with 8; 40 registers and six blocks to
+    // an SM, 22.2.)
+    __device__ __forceinline__ unsigned long long sum(int x, int x1, int step) const
+    {
+        constexpr int kAhead = kFiner ? 4 : 16;
+        unsigned long long sum = 0;
+        for (; x + (kAhead - 1) * step < x1; x += kAhead * step) {
+            float f[kAhead], g[kAhead];
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e) {
+                f[e] = target[x + e * step];
+                g[e] = 0.f;
+                if constexpr (kWhat == Weights::kRest) g[e] = draft[x + e * step];
+            }
+#pragma unroll
+            for (int e = 0; e < kAhead; ++e)
+                if (!(kWhat == Weights::kOthers && x + e * step == gone))
+                    sum += weight<kWhat, kFiner>(f[e], g[e], scale);
+        }
+        for (; x < x1; x += step) sum += at(x);
+        return sum;
+    }
+};
 
 struct Shared {
     unsigned long long warp[kWarps];   // sums of the warps' stretches
-    unsigned long long block[2];       // the block's sum, read by the cluster; one for each try
+    unsigned long long block[2];       // the block's sum, read by the cluster; of two tries in turn
     int accepted;
 };
 
-// Draws from a row's weights: sums, then the token.  Returns false if all are
-// 0.  `turn` counts the calls.
-template <Weights kWhat>
-__device__ __forceinline__ bool draw(const Params& p, const float* target, const float* draft, int gone, float v,
-                                     int rank, int turn, Shared& s, int* next_id)
+// The least sum that a token is drawn from: up to 2^18 weights, cut by a unit at
+// most, then lose 2^-18 of it at most, and half of that on average.
+constexpr unsigned long long kLeast = 1ull << 36;
+// log2 of the finest scale: units of 2^-149, of which every float is a whole number.
+constexpr int kFinest = 105;
+
+// Sums a row's weights and draws a token from them, if the sum is enough or the
+// unit the finest; returns the sum.  `turn` counts the calls.
+template <Weights kWhat, bool kFiner>
+__device__ __forceinline__ unsigned long long try_draw(const Params& p, const Row<kWhat, kFiner>& row, bool finest,
+                                                       float v, int rank, int turn, Shared& s, int* next_id)
 {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int each = ((p.vocab + p.cluster * kWarps - 1) / (p.cluster * kWarps) + 31) / 32 * 32;
     const int x0 = min(p.vocab, (rank * kWarps + warp) * each), x1 = min(p.vocab, x0 + each);
-    const unsigned long long mine = warp_sum(sum_weights<kWhat>(target, draft, gone, x0 + lane, x1, 32));
+    const unsigned long long mine = warp_sum(row.sum(x0 + lane, x1, 32));
+    // (the sums of the try before were read in front of the cluster's barrier there)
     if (lane == 0) s.warp[warp] = mine;
     __syncthreads();
     // every warp knows the sums of those in front of it
     const unsigned long long upto = warp_inclusive_sum(lane < kWarps ? s.warp[lane] : 0ull);
     const unsigned long long block = __shfl_sync(0xffffffffu, upto, 31);
-    if (threadIdx.x == 0) s.block[turn] = block;
+    unsigned long long* given = &s.block[turn & 1];
+    if (threadIdx.x == 0) *given = block;
     __syncwarp();
     cluster_arrive();
     cluster_wait();
     unsigned long long other = 0;
     if (lane < p.cluster) {
         uint32_t at;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(&s.block[turn])), "r"(lane));
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(given)), "r"(lane));
         asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(other) : "r"(at) : "memory");
     }
     const unsigned long long blocks = warp_inclusive_sum(other);
     const unsigned long long sum = __shfl_sync(0xffffffffu, blocks, 31);
-    if (sum == 0) return false;
+    if (sum == 0 || (sum < kLeast && !finest)) return sum;
     // v in units of 2^-64, below 1
     const float below = fminf(v, 0.99999994f) * 18446744073709551616.f;
     const unsigned long long share = v > 0.f ? (unsigned long long)below : 0ull;
     const unsigned long long limit = __umul64hi(sum, share);      // floor(v sum), below sum
     unsigned long long at = __shfl_sync(0xffffffffu, blocks - other, rank) +
                             __shfl_sync(0xffffffffu, upto, warp) - mine;
-    if (limit < at || limit - at >= mine) return true;
+    if (limit < at || limit - at >= mine) return sum;
     // this warp's stretch holds it: a lane sums a piece of neighbours, then the
     // warp scans the piece that holds it
     const int piece = each / 32, p0 = min(x1, x0 + lane * piece), p1 = min(x1, p0 + piece);
-    const unsigned long long own = sum_weights<kWhat>(target, draft, gone, p0, p1, 1);
+    const unsigned long long own = row.sum(p0, p1, 1);
     at += warp_inclusive_sum(own) - own;
     const int holder = __ffs(__ballot_sync(0xffffffffu, limit >= at && limit - at < own)) - 1;
     at = __shfl_sync(0xffffffffu, at, holder);
     const int y1 = __shfl_sync(0xffffffffu, p1, holder);
     for (int y = __shfl_sync(0xffffffffu, p0, holder); y < y1; y += 32) {
-        const unsigned long long w = y + lane < y1 ? weight_of<kWhat>(target, draft, gone, y + lane) : 0ull;
+        const unsigned long long w = y + lane < y1 ? row.at(y + lane) : 0ull;
         const unsigned long long sums = at + warp_inclusive_sum(w);
         const unsigned found = __ballot_sync(0xffffffffu, limit < sums);
         if (found) {
@@ -184,7 +216,40 @@ __device__ __forceinline__ bool draw(const Params& p, const float* target, const
         }
         at = __shfl_sync(0xffffffffu, sums, 31);
     }
-    return true;
+    return sum;
+}
+
+// The tries behind a first one whose sum was not enough; false if all weights are 0.
+// (A function of its own, as it is rare: inside the kernel its registers would
+// be spilled by the first try.)
+template <Weights kWhat>
+__device__ __noinline__ bool draw_finer(const Params& p, const float* target, const float* draft, int gone, float v,
+                                        int rank, int turn, Shared& s, int* next_id, unsigned long long sum)
+{
+    for (int finer = 0; sum < kLeast && finer < kFinest;) {
+        finer = min(kFinest, finer + __clzll((long long)sum) - 20);
+        sum = try_draw(p, Row<kWhat, true>{target, draft, gone, __int_as_float((127 + finer) << 23)}, finer == kFinest,
+                       v, rank, turn++, s, next_id);
+    }
+    __syncwarp();
+    cluster_arrive();      // the blocks' sums have been read, whatever turn comes next
+    cluster_wait();
+    return sum != 0;
+}
+
+// Draws from a row's weights; false if all are 0.  Weights that are small in sum
+// (behind a drafted token that held nearly all of the row) are summed again in
+// units as fine as the sum allows: none of them is above the sum by a unit, so
+// scaled by 2^(44 - bits of the sum) none is above 1, and the sum then has 43 bits
+// at least; a sum of 0 says that all are below a unit.  Every block sees the same
+// sums.  Two rounds where the first finds something, four at most.
+template <Weights kWhat>
+__device__ __forceinline__ bool draw(const Params& p, const float* target, const float* draft, int gone, float v,
+                                     int rank, int& turn, Shared& s, int* next_id)
+{
+    const unsigned long long sum =
+        try_draw(p, Row<kWhat, false>{target, draft, gone, 1.f}, false, v, rank, turn++, s, next_id);
+    return sum >= kLeast || draw_finer<kWhat>(p, target, draft, gone, v, rank, turn, s, next_id, sum);
 }
 
 // A cluster to a request; each block sums a stretch of the row, each warp a
@@ -194,7 +259,8 @@ __device__ __forceinline__ bool draw(const Params& p, const float* target, const
 // probabilities, the rows, the other blocks' sums, the stretch.  One request over
 // 32768 tokens 4.7 us, launch included; 64 over 131071, 17.5 us with the rows in
 // L2, 25 us from HBM (0.40 of copy bandwidth: the chain in front of the rows,
-// which all blocks wait for at the same time, takes 3 us, what follows as long).
+// which all blocks wait for at the same time, takes 3 us, what follows as long);
+// drafted outright 15.8 and 23; with sums that want a second round 29 and 37.
 __global__ void __launch_bounds__(kThreads, 8) draft_verify_kernel(const Params p)
 {
     __shared__ Shared s;
@@ -238,15 +304,12 @@ __global__ void __launch_bounds__(kThreads, 8) draft_verify_kernel(const Params 
     if (row + 1 < b) {
         // the first token that does not stand
         if (p.draft)
-            drawn = draw<Weights::kRest>(p, target, p.draft + (row + 1) * p.draft_stride, -1, v, rank, turn++, s,
+            drawn = draw<Weights::kRest>(p, target, p.draft + (row + 1) * p.draft_stride, -1, v, rank, turn, s,
                                          p.next_ids + i);
-        else drawn = draw<Weights::kOthers>(p, target, nullptr, p.ids[row + 1], v, rank, turn++, s, p.next_ids + i);
+        else drawn = draw<Weights::kOthers>(p, target, nullptr, p.ids[row + 1], v, rank, turn, s, p.next_ids + i);
     }
     // all stand, or nothing is left: the target's row itself
-    if (!drawn) {
-        __syncthreads();      // the sums before these have been read
-        drawn = draw<Weights::kTarget>(p, target, nullptr, -1, v, rank, turn, s, p.next_ids + i);
-    }
+    if (!drawn) drawn = draw<Weights::kTarget>(p, target, nullptr, -1, v, rank, turn, s, p.next_ids + i);
     if (rank == 0 && tid == 0) {
         p.accepted[i] = accepted;
         p.drop[i] = b - a - 1 - accepted;
