@@ -384,8 +384,13 @@ typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
  * tokens of a draft that were not accepted, puts the pages behind the new
  * length, entries ceil(new / page_size) .. ceil(old / page_size) - 1 of its
  * row, on the stack and raises counts[0] by their number (paged_kv_trim does).
- * The next step would take new pages in their place, and they would be lost.  A page stands
- * in one request's row at a time: one in two rows would be given back twice.
+ * The next step would take new pages in their place, and they would be lost.
+ * A page stands in one request's row at a time: one in two rows would be given
+ * back twice.  Entries that name no page of the pool are passed over where a
+ * request's pages are given back (above the count the stack may then hold
+ * anything): pages that no token will see again, behind the window of
+ * paged_attn_window_fwd, may go on the stack while their request lives, once
+ * their entries are set to -1.
  * seq_lens_out may be seq_lens and counts_out may be counts (a loop's state,
  * updated in place); otherwise buffers do not overlap.  Where they are not
  * updated in place the call can be repeated with the same result.
@@ -400,7 +405,7 @@ int paged_kv_plan(const int *seq_lens, const int *new_lens, int n, int *block_ta
 /*
  * Tokens taken back, such as those of a draft that were not accepted: request
  * i keeps its first seq_lens[i] - drop[i] tokens, and the pages behind them go
- * on the free list, requests and pages in order.
+ * on the free list, requests and pages in order, entries of no page left out.
  *   drop         [n] int32 tokens; below 0 counts as 0, above the length as
  *                the length.
  *   seq_lens_out [n] the lengths afterwards; counts_out [2]: free pages
@@ -477,7 +482,8 @@ int paged_attn_fwd(const void *q, const long long *q_strides, const void *k_cach
  * if p - c < window or c < sinks.
  *   window       at least 1; sinks at least 0 (else RA_ERR_INVALID_ARG).
  * The time goes by the keys that are seen.  Pages without a key that some new
- * token sees are not read, nor are their table entries: they may name no page.
+ * token sees are not read, nor are their table entries: they may name no page,
+ * and pages hidden for good may be given back (see paged_kv_plan).
  * Everything else is as in paged_attn_fwd, paged_attn_workspace_size included.
  */
 int paged_attn_window_fwd(const void *q, const long long *q_strides, const void *k_cache,

@@ -113,7 +113,8 @@ def paged_kv_plan(seq_lens, new_lens, block_table, free_list, counts, page_size:
     seq_lens, new_lens [n]; block_table [n, max_pages]; free_list
     [num_pages], a stack whose first counts[0] entries are free; all int32.
     new_lens[i] tokens are added to request i (a negative value ends it);
-    pages go from the stack into block_table, and back, in place.  Returns
+    pages go from the stack into block_table, and back, in place (entries that
+    name no page of the pool are not given back).  Returns
     (seq_lens_out [n], cu_q [n + 1], slots [tokens], counts_out [2]):
     the lengths after the step, where each request's new tokens start, the
     slot of every new token (-1: none) and {free pages, requests not
@@ -142,7 +143,7 @@ def paged_kv_trim(seq_lens, drop, block_table, free_list, counts, page_size: int
                   stream=None):
     """Takes back the last drop[i] tokens of each request (below 0 counts as 0,
     above the length as the length) and puts the pages behind the new lengths
-    on the free list, in place.  All int32, as in paged_kv_plan.  Returns
+    on the free list, in place; table entries that name no page are left out.  All int32, as in paged_kv_plan.  Returns
     (seq_lens_out [n], counts_out [2]): the new lengths and {free pages,
     counts[1]}; seq_lens_out may be seq_lens and counts_out may be counts."""
     dev = _first(block_table, "block_table", 2)
@@ -249,7 +250,8 @@ def paged_attn_window_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_q, wind
     """paged_attn_fwd, causal, with a sliding window: the token at position p
     sees the keys p - window + 1 .. p and the first `sinks` keys of its
     context.  Only their pages are read; table entries of other pages may name
-    none.  window is at least 1."""
+    none, and pages hidden for good may be on the free list again.  window is
+    at least 1."""
     window, sinks = int(window), int(sinks)
     if not (0 < window and 0 <= sinks):
         raise ValueError(f"window must be at least 1 and sinks at least 0, got {window} and {sinks}")

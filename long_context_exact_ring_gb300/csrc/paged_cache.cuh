@@ -4,6 +4,8 @@
 //   paged_append_kernel  new K and V rows into the pool
 #pragma once
 
+#include <type_traits>
+
 #include "paged_index.h"
 #include "paged_ptx.cuh"
 
@@ -15,7 +17,8 @@ constexpr int kPlanThreads = 1024;
 
 // One step's bookkeeping.  With pages(x) = ceil(x / page_size), request i
 // of len_i cached tokens and new_i more:
-//   released pages   r_i = pages(len_i) if new_i < 0, else 0
+//   released pages   r_i = pages(len_i) if new_i < 0, else 0, less the entries
+//                    of those that name no page of the pool
 //   A                F + sum r, F = counts[0], the stack's height
 //   cu_q             exclusive sums of max(new_i, 0)
 //   need_i           pages(len_i + new_i) - pages(len_i), N_i its exclusive sums
@@ -33,6 +36,13 @@ constexpr int kPlanThreads = 1024;
 // requests the 16 blocks cost nothing that shows.  Launch included: 8 requests
 // 8.4 us; 500 requests, 185,000 slots and 0.4 M pages moved 25 us (311 with one
 // block).
+//
+// Entries of no page (a window that hides a page for good lets it go before its
+// request ends) are rare, and to count them takes a look at the released part of
+// the table.  So the scan goes by lengths first and the released entries are
+// stored by them; only where one of them names no page are they counted, a warp to
+// a request, the scan repeated with the counts and the others stored in order
+// (one of 8 requests ends, 1000 pages, 14 us instead of 7.5).
 struct PlanParams {
     const int* seq_lens;
     const int* new_lens;
@@ -113,12 +123,12 @@ __device__ __forceinline__ void cluster_barrier()
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
-// to(request, index) = from(request, index) for the indexes below total of
+// use(request, index, from(request, index)) for the indexes below total of
 // the list whose requests begin at start[0 .. n].  A warp takes as many
 // neighbours as give every warp some, 32 at a time, four reads of a lane in
 // flight: a lane bisects for its first index only and then walks on.
-template <typename From, typename To>
-__device__ __forceinline__ void for_each(int thread, int threads, int n, const int* start, int total, From from, To to)
+template <typename From, typename Use>
+__device__ __forceinline__ void visit(int thread, int threads, int n, const int* start, int total, From from, Use use)
 {
     const int groups = (total + threads - 1) / threads;      // of 32 indexes to a warp
     const long long base = (long long)(thread >> 5) * groups * 32 + (thread & 31);
@@ -139,8 +149,91 @@ __device__ __forceinline__ void for_each(int thread, int threads, int n, const i
         for (int e = 0; e < 4; ++e) value[e] = from(at[e], x[e]);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (k0 + e < groups && base + 32ll * (k0 + e) < total) *to(at[e], x[e]) = value[e];
+            if (k0 + e < groups && base + 32ll * (k0 + e) < total) use(at[e], x[e], value[e]);
     }
+}
+
+// *to(request, index) = from(request, index).
+template <typename From, typename To>
+__device__ __forceinline__ void for_each(int thread, int threads, int n, const int* start, int total, From from, To to)
+{
+    visit(thread, threads, n, start, total, from, [&](int i, int x, int value) { *to(i, x) = value; });
+}
+
+// Is the flag, a variable in shared memory, set in any block of the cluster?
+// Behind a barrier of the cluster; no block may end in front of the next one.
+__device__ __forceinline__ bool any_of_cluster(const int* flag)
+{
+    int value = 0;
+    if ((threadIdx.x & 31) < kPlanCluster) {
+        uint32_t at;
+        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(flag)), "r"(threadIdx.x & 31));
+        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(value) : "r"(at) : "memory");
+    }
+    return __any_sync(0xffffffffu, value);
+}
+
+// Entries [e0, e1) of a table row that name a page of the pool: a warp counts
+// them, or stores them in order at stack + at, in front of stack + end.
+constexpr int kLookAhead = 8;
+__device__ __forceinline__ int count_pages(const int* row, int e0, int e1, int num_pages)
+{
+    int sum = 0;
+    for (int e = e0 + (threadIdx.x & 31); e < e1; e += 32 * kLookAhead) {
+        int page[kLookAhead];
+#pragma unroll
+        for (int x = 0; x < kLookAhead; ++x) page[x] = e < e1 - 32 * x ? row[e + 32 * x] : -1;
+#pragma unroll
+        for (int x = 0; x < kLookAhead; ++x) sum += page_ok(page[x], num_pages);
+    }
+    return (int)__reduce_add_sync(0xffffffffu, (unsigned)sum);
+}
+
+__device__ __forceinline__ void move_pages(const int* row, int e0, int e1, int num_pages, int* stack, int at, int end)
+{
+    const int lane = threadIdx.x & 31;
+    for (int e = e0; e < e1; e += 32 * kLookAhead) {
+        int page[kLookAhead];
+#pragma unroll
+        for (int x = 0; x < kLookAhead; ++x) page[x] = lane < e1 - e - 32 * x ? row[e + 32 * x + lane] : -1;
+#pragma unroll
+        for (int x = 0; x < kLookAhead; ++x) {
+            const bool ok = page_ok(page[x], num_pages);
+            const unsigned some = __ballot_sync(0xffffffffu, ok);
+            const int to = at + __popc(some & ((1u << lane) - 1u));
+            if (ok && to < end) stack[to] = page[x];
+            at += __popc(some);
+        }
+    }
+}
+
+// Stores the entries that are given back, from(request, index) for the indexes
+// below total, at stack + top, in front of its end; then a barrier of the cluster,
+// behind which every block knows whether one of them names no page.  Up to
+// kLookAlone of them every block looks at all; above, at its share, and asks the
+// others, which takes a microsecond more (one of 8 requests ends, plan 7.5 and 8.9
+// us, trim 4.4 and 6.1; 250 of 500, 16.5 us, and each block all of them would take
+// 40 rounds of loads).  *odd is 0.
+constexpr int kLookAlone = 4 * kPlanThreads;
+template <typename From>
+__device__ __forceinline__ bool give_back(long long total, int thread, int threads, int n, const int* start, int num_pages,
+                                          int* stack, int top, int* odd, From from)
+{
+    bool mine = false;
+    const bool alone = total <= kLookAlone, store = !alone || blockIdx.x == 0;
+    if (total > 0) {
+        visit(alone ? threadIdx.x : thread, alone ? kPlanThreads : threads, n, start, (int)total, from,
+              [&](int, int k, int page) {
+                  mine |= !page_ok(page, num_pages);
+                  if (store && k < num_pages - top) stack[top + k] = page;
+              });
+        if (alone) mine = __syncthreads_or(mine);
+        else if (mine) *odd = 1;
+        __syncwarp();
+    }
+    // every block of the cluster has read every length and count, too
+    cluster_barrier();
+    return alone ? mine : any_of_cluster(odd);
 }
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p)
@@ -148,7 +241,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     extern __shared__ int plan_smem_raw[];
     __shared__ long long scratch[64];
     __shared__ unsigned long long s_taken;
-    __shared__ int s_refused;
+    __shared__ int s_refused, s_odd;
     int* s_cu = plan_smem_raw;              // [n + 1] exclusive sums of the new tokens
     int* s_take = s_cu + (p.n + 1);         // [n + 1] exclusive sums of the granted pages
     int* s_rel = s_take + (p.n + 1);        // [n + 1] exclusive sums of the released pages
@@ -161,65 +254,92 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
     auto page_of = [&](int x) { return page_index(x, ps, p.page_shift); };
     auto pages = [&](int x) { return page_of(x + ps - 1); };
     auto length = [&](int i) { return min(max(p.seq_lens[i], 0), capacity); };
-    if (tid == 0) {
-        s_taken = ~0ull;
-        s_refused = 0;
-    }
-
     const int F = min(max(p.counts[0], 0), p.num_pages);
-    long long sums[2] = {0, 0}, totals[2], need_total;      // new tokens, released pages
-    for (int i = i0; i < i1; ++i) {
-        const int q = p.new_lens[i], have = pages(length(i));
-        sums[0] += max(q, 0);
-        sums[1] += q < 0 ? have : 0;
-    }
-    block_exclusive_sums<2>(sums, scratch, totals);
-    const long long add0 = sums[0], rel0 = sums[1], add_total = totals[0], rel_total = totals[1];
-    const long long A = F + rel_total;
-    // pages the request would need: 0 if it does not fit its table row or the slots
-    auto need_of = [&](int q, int len, long long cu, bool* fits) {
-        *fits = q >= 0 && q <= capacity - len && cu + q <= p.tokens;
-        return *fits ? pages(len + q) - pages(len) : 0;
+    long long A, rel_total, need_total;
+    // kCounted: released entries of no page; how many of each request's are left is in s_take.
+    auto scan = [&](auto counted) {
+        constexpr bool kCounted = decltype(counted)::value;
+        if (tid == 0) {
+            s_taken = ~0ull;
+            s_refused = 0;
+        }
+        auto given_back = [&](int i, int len) { return kCounted ? s_take[i] : pages(len); };
+        long long sums[2] = {0, 0}, totals[2];      // new tokens, released pages
+        for (int i = i0; i < i1; ++i) {
+            const int q = p.new_lens[i];
+            sums[0] += max(q, 0);
+            sums[1] += q < 0 ? given_back(i, length(i)) : 0;
+        }
+        block_exclusive_sums<2>(sums, scratch, totals);
+        const long long add0 = sums[0], add_total = totals[0];
+        long long released = sums[1];
+        rel_total = totals[1];
+        A = F + rel_total;
+        // pages the request would need: 0 if it does not fit its table row or the slots
+        auto need_of = [&](int q, int len, long long cu, bool* fits) {
+            *fits = q >= 0 && q <= capacity - len && cu + q <= p.tokens;
+            return *fits ? pages(len + q) - pages(len) : 0;
+        };
+        long long need = 0, cu = add0;
+        for (int i = i0; i < i1; ++i) {
+            bool fits;
+            const int q = p.new_lens[i];
+            need += need_of(q, length(i), cu, &fits);
+            cu += max(q, 0);
+        }
+        long long before = block_exclusive_sum(need, scratch, &need_total);
+        int refused = 0;
+        cu = add0;
+        for (int i = i0; i < i1; ++i) {
+            bool fits;
+            const int q = p.new_lens[i], len = length(i);
+            const int want = need_of(q, len, cu, &fits), back = q < 0 ? given_back(i, len) : 0;
+            const bool granted = fits && (want == 0 || before + want <= A);
+            s_cu[i] = (int)min(cu, (long long)INT_MAX);
+            s_take[i] = (int)min(before, A);     // requests past A get nothing
+            s_rel[i] = (int)released;
+            s_len[i] = granted ? len : ~len;
+            refused += q >= 0 && !granted;
+            // pages handed out are those before the first request that goes without
+            if (fits && !granted) atomicMin(&s_taken, (unsigned long long)before);
+            before += want;
+            cu += max(q, 0);
+            released += back;
+        }
+        if (refused) atomicAdd(&s_refused, refused);
+        if (tid == 0) {
+            s_cu[n] = (int)min(add_total, (long long)INT_MAX);
+            s_take[n] = (int)min(need_total, A);
+            s_rel[n] = (int)rel_total;
+        }
+        __syncthreads();
     };
-    long long need = 0, cu = add0;
-    for (int i = i0; i < i1; ++i) {
-        bool fits;
-        const int q = p.new_lens[i];
-        need += need_of(q, length(i), cu, &fits);
-        cu += max(q, 0);
+    if (tid == 0) s_odd = 0;
+    scan(std::false_type{});
+    // the released pages go on the stack, above all that is read of it
+    const bool holes =
+        give_back(rel_total, thread, threads, n, s_rel, p.num_pages, p.free_list, F, &s_odd,
+                  [&](int j, int k) { return p.table[j * p.table_stride + (k - s_rel[j])]; });
+    if (holes) {
+        for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {
+            const int c = p.new_lens[i] < 0
+                              ? count_pages(p.table + i * p.table_stride, 0, pages(length(i)), p.num_pages) : 0;
+            __syncwarp();
+            if ((tid & 31) == 0) s_take[i] = c;
+        }
+        __syncthreads();
+        scan(std::true_type{});
+        for (int i = thread >> 5; i < n; i += threads / 32)
+            if (p.new_lens[i] < 0)
+                move_pages(p.table + i * p.table_stride, 0, pages(length(i)), p.num_pages, p.free_list, F + s_rel[i],
+                           p.num_pages);
+        cluster_barrier();      // as above, and the stack is complete
     }
-    long long before = block_exclusive_sum(need, scratch, &need_total), released = rel0;
-    int refused = 0;
-    cu = add0;
-    for (int i = i0; i < i1; ++i) {
-        bool fits;
-        const int q = p.new_lens[i], len = length(i);
-        const int want = need_of(q, len, cu, &fits);
-        const bool granted = fits && (want == 0 || before + want <= A);
-        s_cu[i] = (int)min(cu, (long long)INT_MAX);
-        s_take[i] = (int)min(before, A);     // requests past A get nothing
-        s_rel[i] = (int)released;
-        s_len[i] = granted ? len : ~len;
-        refused += q >= 0 && !granted;
-        // pages handed out are those before the first request that goes without
-        if (fits && !granted) atomicMin(&s_taken, (unsigned long long)before);
-        before += want;
-        cu += max(q, 0);
-        if (q < 0) released += pages(len);
-    }
-    if (refused) atomicAdd(&s_refused, refused);
-    if (tid == 0) {
-        s_cu[n] = (int)min(add_total, (long long)INT_MAX);
-        s_take[n] = (int)min(need_total, A);
-        s_rel[n] = (int)rel_total;
-    }
-    __syncthreads();
-    // every block of the cluster has read every input length and count
-    cluster_barrier();
     const int taken = (int)min((long long)min(s_taken, (unsigned long long)need_total), A);
 
     // A page of the stack, as it stands after the releases.
     auto stack = [&](int x) {
+        if (holes) return x < p.num_pages ? __ldcg(p.free_list + x) : -1;
         if (x < F) return p.free_list[x];
         const int j = find_last_le(s_rel, n, x - F);
         return p.table[j * p.table_stride + (x - F - s_rel[j])];
@@ -237,10 +357,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
             p.counts_out[1] = s_refused;
         }
     }
-    for_each(
-        thread, threads, n, s_rel, (int)min(rel_total, (long long)p.num_pages - F),
-        [&](int j, int k) { return p.table[j * p.table_stride + (k - s_rel[j])]; },
-        [&](int, int k) { return p.free_list + F + k; });
     for_each(
         thread, threads, n, s_take, taken, [&](int, int k) { return stack((int)A - 1 - k); },
         [&](int i, int k) { return p.table + i * p.table_stride + pages(s_len[i]) + (k - s_take[i]); });
@@ -260,11 +376,12 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
 }
 
 // Tokens taken back: request i keeps len_i - drop_i of its tokens, and the
-// pages behind them go on the stack, in order of requests and of pages.  As in
-// paged_plan_kernel one cluster, every block with the whole scan and a share
-// of the stores, the barrier between reads and stores so that outputs may
-// alias inputs.  Launch included: 8 requests 3.1 us; 500 requests and 0.16 M
-// pages 8 us, of which 5 are the chain of lengths, scan, barrier, entries.
+// pages behind them go on the stack, in order of requests and of pages; entries
+// of no page as in paged_plan_kernel.  As there one cluster, every block with the
+// whole scan and a share of the stores, the barrier between reads and stores so
+// that outputs may alias inputs.  Launch included: 8 requests 3.0 us, with 500
+// pages 4.4; 500 requests and 0.13 M pages 10 us, a chain of lengths, scan,
+// entries, barrier, the other blocks' flags.
 struct TrimParams {
     const int* seq_lens;
     const int* drop;
@@ -284,6 +401,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
 {
     extern __shared__ int trim_smem_raw[];
     __shared__ long long scratch[32];
+    __shared__ int s_odd;
     int* s_rel = trim_smem_raw;             // [n + 1] exclusive sums of the pages given back
     int* s_first = s_rel + (p.n + 1);       // [n] the first of them
     const int tid = threadIdx.x, n = p.n;
@@ -300,6 +418,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
         s_first[i] = pages(after);
         mine += pages(len) - pages(after);
     }
+    if (tid == 0) s_odd = 0;
     long long before = block_exclusive_sum(mine, scratch, &total);
     for (int i = i0; i < i1; ++i) {
         s_rel[i] = (int)before;
@@ -307,8 +426,31 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
     }
     if (tid == 0) s_rel[n] = (int)total;
     __syncthreads();
-    // every block of the cluster has read every length and count
-    cluster_barrier();
+    const bool asked = total > kLookAlone;
+    const bool holes =
+        give_back(total, thread, threads, n, s_rel, p.num_pages, p.free_list, F, &s_odd,
+                  [&](int j, int k) { return p.table[j * p.table_stride + s_first[j] + (k - s_rel[j])]; });
+    if (holes) {
+        for (int i = tid >> 5; i < n; i += kPlanThreads / 32) {
+            const int c = count_pages(p.table + i * p.table_stride, s_first[i], pages(length(i)), p.num_pages);
+            if ((tid & 31) == 0) s_rel[i] = c;
+        }
+        __syncthreads();
+        mine = 0;
+        for (int i = i0; i < i1; ++i) mine += s_rel[i];
+        before = block_exclusive_sum(mine, scratch, &total);
+        for (int i = i0; i < i1; ++i) {
+            const int c = s_rel[i];
+            s_rel[i] = (int)before;
+            before += c;
+        }
+        __syncthreads();
+        for (int i = thread >> 5; i < n; i += threads / 32)
+            move_pages(p.table + i * p.table_stride, s_first[i], pages(length(i)), p.num_pages, p.free_list,
+                       F + s_rel[i], p.num_pages);
+        cluster_barrier();      // as above
+    }
+    if (asked) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");      // no block has to be asked any more
     const int moved = (int)min(total, (long long)p.num_pages - F);
     if (blockIdx.x == 0) {
         for (int i = i0; i < i1; ++i) {
@@ -320,10 +462,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
             p.counts_out[1] = other;
         }
     }
-    for_each(
-        thread, threads, n, s_rel, moved,
-        [&](int j, int k) { return p.table[j * p.table_stride + s_first[j] + (k - s_rel[j])]; },
-        [&](int, int k) { return p.free_list + F + k; });
+    __syncwarp();
+    if (asked) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // K and V rows of the new tokens to their slots; every thread moves 16 bytes
