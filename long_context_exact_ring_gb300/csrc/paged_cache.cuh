@@ -42,7 +42,7 @@ constexpr int kPlanThreads = 1024;
 // the table.  So the scan goes by lengths first and the released entries are
 // stored by them; only where one of them names no page are they counted, a warp to
 // a request, the scan repeated with the counts and the others stored in order
-// (one of 8 requests ends, 1000 pages, 14 us instead of 7.5).
+// (one of 8 requests ends, 1000 pages, 14 us instead of 7.8).
 struct PlanParams {
     const int* seq_lens;
     const int* new_lens;
@@ -117,11 +117,17 @@ __device__ __forceinline__ int find_last_le(const int* a, int n, int x)
 
 constexpr int kPlanCluster = 16;
 
-// Barrier of all threads of the cluster, with what they wrote before it.
+// Barrier of all threads of the cluster, with what they wrote before it, in one
+// or in two.
 __device__ __forceinline__ void cluster_barrier()
 {
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
+__device__ __forceinline__ void cluster_barrier_begin()
+{
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_barrier_end() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 // use(request, index, from(request, index)) for the indexes below total of
 // the list whose requests begin at start[0 .. n].  A warp takes as many
@@ -160,17 +166,17 @@ __device__ __forceinline__ void for_each(int thread, int threads, int n, const i
     visit(thread, threads, n, start, total, from, [&](int i, int x, int value) { *to(i, x) = value; });
 }
 
-// Is the flag, a variable in shared memory, set in any block of the cluster?
-// Behind a barrier of the cluster; no block may end in front of the next one.
-__device__ __forceinline__ bool any_of_cluster(const int* flag)
+// Sets the flag, a variable in shared memory, in every block of the cluster.  A
+// warp calls it, in front of a barrier of the cluster and behind one that
+// followed the flag's first value.
+__device__ __forceinline__ void set_in_cluster(const int* flag)
 {
-    int value = 0;
     if ((threadIdx.x & 31) < kPlanCluster) {
         uint32_t at;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(flag)), "r"(threadIdx.x & 31));
-        asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(value) : "r"(at) : "memory");
+        asm volatile("st.shared::cluster.s32 [%0], 1;" ::"r"(at) : "memory");
     }
-    return __any_sync(0xffffffffu, value);
+    __syncwarp();
 }
 
 // Entries [e0, e1) of a table row that name a page of the pool: a warp counts
@@ -210,10 +216,9 @@ __device__ __forceinline__ void move_pages(const int* row, int e0, int e1, int n
 // Stores the entries that are given back, from(request, index) for the indexes
 // below total, at stack + top, in front of its end; then a barrier of the cluster,
 // behind which every block knows whether one of them names no page.  Up to
-// kLookAlone of them every block looks at all; above, at its share, and asks the
-// others, which takes a microsecond more (one of 8 requests ends, plan 7.5 and 8.9
-// us, trim 4.4 and 6.1; 250 of 500, 16.5 us, and each block all of them would take
-// 40 rounds of loads).  *odd is 0.
+// kLookAlone of them every block looks at all; above, at its share, and tells the
+// others (4096 pages of 8 requests, trim 4.8 us, shared 5.1; 8192, 5.1, each block
+// all of them 6.0).  *odd is 0, behind a barrier of the block.
 constexpr int kLookAlone = 4 * kPlanThreads;
 template <typename From>
 __device__ __forceinline__ bool give_back(long long total, int thread, int threads, int n, const int* start, int num_pages,
@@ -221,6 +226,7 @@ __device__ __forceinline__ bool give_back(long long total, int thread, int threa
 {
     bool mine = false;
     const bool alone = total <= kLookAlone, store = !alone || blockIdx.x == 0;
+    if (!alone) cluster_barrier_begin();
     if (total > 0) {
         visit(alone ? threadIdx.x : thread, alone ? kPlanThreads : threads, n, start, (int)total, from,
               [&](int, int k, int page) {
@@ -228,12 +234,15 @@ __device__ __forceinline__ bool give_back(long long total, int thread, int threa
                   if (store && k < num_pages - top) stack[top + k] = page;
               });
         if (alone) mine = __syncthreads_or(mine);
-        else if (mine) *odd = 1;
-        __syncwarp();
+    }
+    __syncwarp();
+    if (!alone) {
+        cluster_barrier_end();      // every block has its flag
+        if (__any_sync(0xffffffffu, mine)) set_in_cluster(odd);
     }
     // every block of the cluster has read every length and count, too
     cluster_barrier();
-    return alone ? mine : any_of_cluster(odd);
+    return alone ? mine : *odd != 0;
 }
 
 __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanParams p)
@@ -380,8 +389,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(const PlanPara
 // of no page as in paged_plan_kernel.  As there one cluster, every block with the
 // whole scan and a share of the stores, the barrier between reads and stores so
 // that outputs may alias inputs.  Launch included: 8 requests 3.0 us, with 500
-// pages 4.4; 500 requests and 0.13 M pages 10 us, a chain of lengths, scan,
-// entries, barrier, the other blocks' flags.
+// pages 4.4; 500 requests and 0.13 M pages 8.5 us, a chain of lengths, scan,
+// entries, barrier.
 struct TrimParams {
     const int* seq_lens;
     const int* drop;
@@ -411,6 +420,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
     const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
     auto pages = [&](int x) { return page_index(x + p.page_size - 1, p.page_size, p.page_shift); };
     auto length = [&](int i) { return min(max(p.seq_lens[i], 0), capacity); };
+    if (tid == 0) s_odd = 0;
     const int F = min(max(p.counts[0], 0), p.num_pages), other = p.counts[1];
     long long mine = 0, total;
     for (int i = i0; i < i1; ++i) {
@@ -418,7 +428,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
         s_first[i] = pages(after);
         mine += pages(len) - pages(after);
     }
-    if (tid == 0) s_odd = 0;
     long long before = block_exclusive_sum(mine, scratch, &total);
     for (int i = i0; i < i1; ++i) {
         s_rel[i] = (int)before;
@@ -426,7 +435,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
     }
     if (tid == 0) s_rel[n] = (int)total;
     __syncthreads();
-    const bool asked = total > kLookAlone;
     const bool holes =
         give_back(total, thread, threads, n, s_rel, p.num_pages, p.free_list, F, &s_odd,
                   [&](int j, int k) { return p.table[j * p.table_stride + s_first[j] + (k - s_rel[j])]; });
@@ -450,7 +458,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
                        F + s_rel[i], p.num_pages);
         cluster_barrier();      // as above
     }
-    if (asked) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");      // no block has to be asked any more
     const int moved = (int)min(total, (long long)p.num_pages - F);
     if (blockIdx.x == 0) {
         for (int i = i0; i < i1; ++i) {
@@ -462,8 +469,6 @@ __global__ void __launch_bounds__(kPlanThreads) paged_trim_kernel(const TrimPara
             p.counts_out[1] = other;
         }
     }
-    __syncwarp();
-    if (asked) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // K and V rows of the new tokens to their slots; every thread moves 16 bytes
