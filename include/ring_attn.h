@@ -504,7 +504,7 @@ int paged_attn_window_fwd(const void *q, const long long *q_strides, const void 
  * inv_freq[i]) and s_i the same of the sine; elements from rot_dim on stay as
  * they are (normed, where there is a norm).  Pair i is (i, i + rot_dim / 2), or (2i,
  * 2i + 1) with interleaved = 1.  Computed in fp32 from one reading of x and
- * rounded once; the angle is reduced exactly, for any 32-bit position.
+ * rounded once; angles are reduced to 2^-33 of a turn, at any 32-bit position.
  *   q_weight, k_weight  [d] fp32, NULL: no norm of that tensor.
  *   eps          finite, not negative; unused without weights.
  *   inv_freq     [rot_dim / 2] fp32, finite, below 2^26.

@@ -76,14 +76,17 @@ struct Paged {
 
 // f / (2 pi) modulo 1, in units of 2^-64 of a turn: a position's angle is then
 // a product modulo 2^64, exact to 2^-64 of a turn for each position, however
-// far.  f = m 2^-s is multiplied by 2^66 / (2 pi), rounded.
+// far.  f = m 2^-s, below 2^26, is multiplied by 2^130 / (2 pi) in two words: with
+// one, 2^66 / (2 pi), frequencies from 2^8 on would be off by more than a unit,
+// those near 2^26 by 2^18 of them.
 __device__ __forceinline__ uint64_t turn_of(float f)
 {
-    constexpr uint64_t kTurn = 0xa2f9836e4e44152aull;
+    constexpr uint64_t kTurn = 0xa2f9836e4e441529ull, kRest = 0xfc2757d1f534ddc0ull;
     const uint32_t bits = __float_as_uint(f);
     const uint32_t e = max(bits >> 23 & 255u, 1u);
     const uint64_t m = (bits & 0x7fffffu) | (bits & 0x7f800000u ? 0x800000u : 0u);
-    const uint64_t lo = m * kTurn, hi = __umul64hi(m, kTurn);
+    const uint64_t carried = __umul64hi(m, kRest), lo = m * kTurn + carried;
+    const uint64_t hi = __umul64hi(m, kTurn) + (lo < carried);
     const int shift = 152 - (int)e;
     uint64_t t = 0;
     if (shift >= 64) t = shift < 128 ? hi >> (shift - 64) : 0ull;
