@@ -29,7 +29,12 @@ def rope_inv_freq(rot_dim: int, base: float = 10000.0, *, scaling: str | None = 
              "parts"   (YaRN, arXiv 2309.00071) those with fewer than
                        beta_slow turns over original_length are divided by
                        factor, those with more than beta_fast stay, between
-                       them a mixture; the amplitude is 0.1 ln(factor) + 1"""
+                       them a mixture, linear in the turns as the paper has
+                       it; the amplitude is 0.1 ln(factor) + 1.  Many models
+                       of that name are trained with a mixture linear in the
+                       pair's index instead, whose frequencies differ by up
+                       to a factor of several: for those pass their own
+                       inv_freq, which may be any tensor"""
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError(f"rot_dim must be a positive even number, got {rot_dim}")
     if not (base > 1.0 and math.isfinite(base) and factor >= 1.0 and math.isfinite(factor)):
