@@ -144,7 +144,9 @@ def qk_norm_rope_bwd(dq, dk, q, k, positions, inv_freq, *, q_weight=None, k_weig
     """Gradients of qk_norm_rope_fwd's q, k and weights from those of its
     outputs: (dq_in, dk_in, dq_weight, dk_weight), the last two [d] fp32, or
     None where there is no weight.  dq_in and dk_in default to the layouts of q
-    and k, and may be dq and dk.  The same call gives the same bits."""
+    and k, and may be dq and dk.  q (k) gives the shapes; without its weight its
+    values are not read, so that any tensor of its shape, dq (dk) itself too,
+    will do.  The same call gives the same bits."""
     dev = _first(q, "q", 4)
     dtype = _typed(q, "q")
     B, H, S, d = q.shape

@@ -16,9 +16,10 @@ int check_rope(int dtype, int heads_a, int heads_b, int d, int rot, int interlea
     return RA_OK;
 }
 
-// Shares of a token's `rows` rows: one where the tokens alone occupy the warps,
-// else as many as that takes, of at least one row to a lane group (a decode
-// token, 32 heads over 8: 4.0 us, with whole batches 4.7).
+// Shares of a token's `rows` rows: one where the tokens alone occupy the warps of
+// the forward kernel, else as many as that takes, of at least one row to a lane
+// group (a decode token, 32 heads over 8: 4.0 us, with whole batches 4.7).  The
+// backward kernel takes the same shares with three quarters of the warps.
 int rope_parts(int tokens, int rows, int d, int sms)
 {
     const int step = 512 / d;

@@ -39,3 +39,16 @@ def test_rows_and_weights(ra, shape, dtype, interleaved, norm):
         if w[n] is not None:
             dw, tol, _ = weight_grad_and_tol(x["d" + n], x[n], w[n], *args)
             assert_close(got[2 + i], dw, tol, "weight of " + n)
+
+
+@pytest.mark.parametrize("shape", SHAPES[1:4])
+def test_rows_are_not_read_without_weights(ra, shape):
+    """The gradients themselves may stand for them."""
+    x = case(shape, torch.bfloat16)
+    q, k, dq, dk = [x[n].cuda() for n in ("q", "k", "dq", "dk")]
+    at = (x["pos"].cuda(), x["freq"].cuda())
+    want = ra.qk_norm_rope_bwd(dq, dk, q, k, *at)
+    got = ra.qk_norm_rope_bwd(dq, dk, dq, dk, *at)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and got[2] is None and got[3] is None
+    got = ra.qk_norm_rope_bwd(dq, dk, dq, dk, *at, dq_in=dq, dk_in=dk)
+    assert got[0] is dq and torch.equal(dq, want[0]) and torch.equal(dk, want[1])
