@@ -390,7 +390,9 @@ typedef enum { RA_BF16 = 0, RA_FP16 = 1 } ra_dtype;
  * request's pages are given back (above the count the stack may then hold
  * anything): pages that no token will see again, behind the window of
  * paged_attn_window_fwd, may go on the stack while their request lives, once
- * their entries are set to -1.
+ * their entries are set to -1.  (The rows of a request that is not granted
+ * stand at the last tokens that it holds and see further back, as do those
+ * behind tokens taken back: keep as many keys more.)
  * seq_lens_out may be seq_lens and counts_out may be counts (a loop's state,
  * updated in place); otherwise buffers do not overlap.  Where they are not
  * updated in place the call can be repeated with the same result.
